@@ -1,5 +1,6 @@
 """Python binding of libnq: linear layers with a low-rank binary-factorised weight
-W_hat = diag(s1) U diag(g) V^T diag(s2) on MI355X.
+W_hat = diag(s1) U diag(g) V^T diag(s2) on MI355X, and what stands beside them in a
+model: linears with 4-bit weights (q4_*) and the norms between blocks (block_norm).
 
 Argument marshalling only: every step of the forward runs in the HIP kernels of
 libnq.so, reached through its C ABI (include/nq.h).  PyTorch provides device
@@ -16,11 +17,12 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libnq.so")
 
-NQ_OK, NQ_ERR_INVALID_ARG, NQ_ERR_NOT_PM1, NQ_ERR_WORKSPACE, NQ_ERR_UNSUPPORTED, NQ_ERR_HIP, NQ_ERR_INTERNAL = \
-    0, -1, -2, -3, -4, -5, -6
+NQ_OK, NQ_ERR_INVALID_ARG, NQ_ERR_NOT_PM1, NQ_ERR_WORKSPACE, NQ_ERR_UNSUPPORTED, NQ_ERR_HIP, NQ_ERR_INTERNAL, \
+    NQ_ERR_RANGE = 0, -1, -2, -3, -4, -5, -6, -7
 NQ_F32, NQ_F16, NQ_BF16 = 0, 1, 2
 NQ_GROUP_MAX = 4  # layers per group call (include/nq.h)
 NQ_ENVELOPE_MAX = 4  # terms of a rank-l envelope (include/nq.h)
+NQ_NORM_POST, NQ_NORM_PRE, NQ_NORM_MAX_DIM = 1, 2, 32768  # block norms (include/nq.h)
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "valu": 3, "decode": 4}
 
 _DT = {torch.float32: NQ_F32, torch.float16: NQ_F16, torch.bfloat16: NQ_BF16}
@@ -37,6 +39,18 @@ class nq_layer(ctypes.Structure):
                 ("scale_dtype", ctypes.c_int32), ("blob", ctypes.c_void_p)]
 
 
+class nq_q4_layer(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int32), ("n", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32), ("zeros", ctypes.c_int32), ("blob", ctypes.c_void_p)]
+
+
+class nq_block_norm(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("flags", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("block_scale", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -49,7 +63,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing; build it with `python -m binary_rank_gemv_packed_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
     c_int, c_size, vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
-    P = ctypes.POINTER(nq_layer)
+    P, Q, N = ctypes.POINTER(nq_layer), ctypes.POINTER(nq_q4_layer), ctypes.POINTER(nq_block_norm)
     sigs = {
         "nq_abi_version": (c_int, []),
         "nq_layer_bytes": (c_size, [c_int, c_int, c_int, c_int]),
@@ -74,6 +88,16 @@ def lib() -> ctypes.CDLL:
         "nq_admm_factorize": (c_int, [vp, c_int, c_int, c_int, vp, vp, ctypes.c_float, c_int, c_int, vp, vp, vp, vp,
                                       vp, vp, vp, c_size, vp]),
         "nq_balance_scales": (c_int, [vp, vp, vp, c_int, c_int, c_int, vp]),
+        "nq_q4_layer_bytes": (c_size, [c_int, c_int, c_int, c_int, c_int]),
+        "nq_q4_pack": (c_int, [Q, vp, vp, vp, vp]),
+        "nq_q4_unpack": (c_int, [Q, vp, vp, vp]),
+        "nq_q4_workspace_bytes": (c_size, [Q, c_int]),
+        "nq_q4_linear_fwd": (c_int, [Q, vp, c_int, vp, c_int, c_int, vp, c_size, vp]),
+        "nq_q4_workspace_bytes_group": (c_size, [vp, c_int, c_int]),
+        "nq_q4_linear_fwd_group": (c_int, [vp, c_int, vp, c_int, vp, c_int, c_int, vp, c_size, vp]),
+        "nq_block_norm_fwd": (c_int, [N, c_int, vp, vp, vp, vp, vp, vp, vp]),
+        "nq_block_norm_workspace_bytes": (c_size, [N, c_int]),
+        "nq_block_norm_bwd": (c_int, [N, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_size, vp]),
         "nq_bits_per_weight": (ctypes.c_double, [c_int, c_int, c_int, c_int]),
         "nq_rank_for_bits": (c_int, [c_int, c_int, ctypes.c_double, c_int]),
         "nq_status_string": (ctypes.c_char_p, [c_int]),
@@ -95,6 +119,25 @@ def _check(status: int) -> None:
 def _stream(stream=None) -> int:
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _on_stream(device: torch.device, stream, call):
+    """call(raw stream) with `device` current: on the given stream, else on the
+    device's current one.  What call allocates belongs to that stream."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(device):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if s.device != device:
+            raise NQError(NQ_ERR_INVALID_ARG, f"stream on {s.device}, tensors on {device}")
+        with torch.cuda.stream(s):
+            return call(s.cuda_stream)
+
+
+def _gpu_tensor(t: torch.Tensor, name: str, dtype, shape, device) -> None:
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise NQError(NQ_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                                          f"{device} (got {t.dtype} {tuple(t.shape)} on {t.device})")
 
 
 class Layer:
@@ -363,6 +406,283 @@ def balance_scales(s1: torch.Tensor, g: torch.Tensor, s2: torch.Tensor, stream=N
             raise NQError(NQ_ERR_INVALID_ARG, "s1, g and s2 must be contiguous fp32 GPU tensors")
     _check(lib().nq_balance_scales(s1.data_ptr(), g.data_ptr(), s2.data_ptr(), s1.numel(), s2.numel(), g.numel(),
                                    _stream(stream)))
+
+
+# ------------------------------------------------------------------ 4-bit linears
+class Q4Layer:
+    """A packed 4-bit layer: the device blob plus its dimensions."""
+
+    def __init__(self, m: int, n: int, group: int, scale_dtype: torch.dtype, zeros: bool, blob: torch.Tensor):
+        self.m, self.n, self.group, self.scale_dtype, self.zeros, self.blob = m, n, group, scale_dtype, zeros, blob
+        self.c = nq_q4_layer(m, n, group, _DT[scale_dtype], int(zeros), blob.data_ptr())
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    @property
+    def device(self):
+        return self.blob.device
+
+
+class Q4Group:
+    """4-bit layers that read the same x (q, k and v; gate and up): same n, group,
+    scale dtype and kind of zero point, on one device."""
+
+    def __init__(self, layers):
+        self.layers = list(layers)
+        if not 1 <= len(self.layers) <= NQ_GROUP_MAX or len({L.device for L in self.layers}) != 1:
+            raise NQError(NQ_ERR_INVALID_ARG, f"a group holds 1..{NQ_GROUP_MAX} layers on one device")
+        self.n, self.device = self.layers[0].n, self.layers[0].device
+        self._refs = (ctypes.POINTER(nq_q4_layer) * len(self.layers))(*[ctypes.pointer(L.c) for L in self.layers])
+        self.ref = ctypes.cast(self._refs, ctypes.c_void_p)
+
+    def __len__(self):
+        return len(self.layers)
+
+
+def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None, group: int = 128,
+            stream=None) -> Q4Layer:
+    """Packs the 4-bit weight W[i, j] = scales[i, j // group] * (codes[i, j] -
+    zeros[i, j // group]) already on the GPU: codes uint8 (m, n) in 0..15, scales
+    fp16 or fp32 (m, ceil(n / group)), zeros uint8 of that shape in 0..15 or None
+    for 8 everywhere; group 32, 64 or 128.  Blocks until validation is done."""
+    if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_cuda:
+        raise NQError(NQ_ERR_INVALID_ARG, "codes must be a uint8 GPU matrix")
+    if scales.dtype not in (torch.float16, torch.float32):
+        raise NQError(NQ_ERR_INVALID_ARG, "scales must be fp16 or fp32")
+    m, n = codes.shape
+    nbytes = int(lib().nq_q4_layer_bytes(m, n, group, _DT[scales.dtype], int(zeros is not None)))
+    if nbytes == 0:
+        raise NQError(NQ_ERR_INVALID_ARG, f"invalid 4-bit layer m={m} n={n} group={group}")
+
+    def call(s):
+        c, sc = codes.contiguous(), scales.contiguous()
+        z = zeros.contiguous() if zeros is not None else None
+        shape = torch.Size((m, (n + group - 1) // group))
+        _gpu_tensor(sc, "scales", scales.dtype, shape, codes.device)
+        if z is not None:
+            _gpu_tensor(z, "zeros", torch.uint8, shape, codes.device)
+        layer = Q4Layer(m, n, group, scales.dtype, z is not None,
+                        torch.empty(nbytes, dtype=torch.uint8, device=codes.device))
+        _check(lib().nq_q4_pack(layer.ref, c.data_ptr(), sc.data_ptr(), z.data_ptr() if z is not None else None, s))
+        return layer
+
+    return _on_stream(codes.device, stream, call)
+
+
+def q4_unpack(layer: Q4Layer, stream=None):
+    """(codes, zeros or None) read back from the packed blob, as q4_pack took them."""
+    def call(s):
+        codes = torch.empty((layer.m, layer.n), dtype=torch.uint8, device=layer.device)
+        zeros = torch.empty((layer.m, (layer.n + layer.group - 1) // layer.group), dtype=torch.uint8,
+                            device=layer.device) if layer.zeros else None
+        _check(lib().nq_q4_unpack(layer.ref, codes.data_ptr(), zeros.data_ptr() if layer.zeros else None, s))
+        return codes, zeros
+
+    return _on_stream(layer.device, stream, call)
+
+
+def q4_workspace_bytes(layer, B: int) -> int:
+    """Workspace of q4_linear_into (a Q4Layer) or q4_linear_group_into (a Q4Group
+    or a list of layers) for batch B."""
+    if isinstance(layer, Q4Layer):
+        return int(lib().nq_q4_workspace_bytes(layer.ref, B))
+    group = layer if isinstance(layer, Q4Group) else Q4Group(layer)
+    return int(lib().nq_q4_workspace_bytes_group(group.ref, len(group), B))
+
+
+def new_q4_workspace(layer, B: int) -> torch.Tensor:
+    device = layer.device if isinstance(layer, (Q4Layer, Q4Group)) else layer[0].device
+    return torch.empty(max(q4_workspace_bytes(layer, B), 256), dtype=torch.uint8, device=device)
+
+
+def _q4_batch(x: torch.Tensor, n: int, device) -> int:
+    if x.dtype not in (torch.bfloat16, torch.float32) or x.device != device or not x.is_contiguous() or \
+            x.dim() not in (1, 2) or x.shape[-1] != n:
+        raise NQError(NQ_ERR_INVALID_ARG, f"x must be contiguous bf16 or fp32 of shape (B, {n}) or ({n},) on {device}")
+    return x.shape[0] if x.dim() == 2 else 1
+
+
+def _q4_output(x: torch.Tensor, B: int, y: torch.Tensor, m: int, dtype: torch.dtype) -> None:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise NQError(NQ_ERR_INVALID_ARG, "y must be bf16 or fp32")
+    _gpu_tensor(y, "y", dtype, (B, m) if x.dim() == 2 else (m,), x.device)
+
+
+def _q4_scratch(workspace: torch.Tensor, device) -> None:
+    _gpu_tensor(workspace, "the workspace", torch.uint8, (workspace.numel(),), device)
+
+
+def q4_linear_into(x: torch.Tensor, layer: Q4Layer, y: torch.Tensor, workspace: torch.Tensor,
+                   stream=None) -> torch.Tensor:
+    """y = x W^T into caller buffers, x (B, n) or (n,) bf16 or fp32, y (B, m) or
+    (m,); enqueues on the stream and returns without synchronising (safe to
+    capture in a graph)."""
+    B = _q4_batch(x, layer.n, layer.device)
+    _q4_output(x, B, y, layer.m, y.dtype)
+    _q4_scratch(workspace, layer.device)
+    _on_stream(layer.device, stream, lambda s: _check(lib().nq_q4_linear_fwd(
+        layer.ref, x.data_ptr(), _DT[x.dtype], y.data_ptr(), _DT[y.dtype], B, workspace.data_ptr(),
+        workspace.numel(), s)))
+    return y
+
+
+def q4_linear(x: torch.Tensor, layer: Q4Layer, out_dtype: torch.dtype | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x W^T for x of shape (B, n) or (n,); y has x's dtype unless given."""
+    def call(_):
+        xx = x.contiguous()
+        B = _q4_batch(xx, layer.n, layer.device)
+        y = torch.empty((*xx.shape[:-1], layer.m), dtype=out_dtype or x.dtype, device=x.device)
+        ws = workspace if workspace is not None else new_q4_workspace(layer, B)
+        return q4_linear_into(xx, layer, y, ws)
+
+    return _on_stream(layer.device, stream, call)
+
+
+def q4_linear_group_into(x: torch.Tensor, layers, ys, workspace: torch.Tensor, stream=None):
+    """ys[l] = x W_l^T for 4-bit layers sharing x (a Q4Group, or a list of
+    layers); one launch for all of them up to B = 16."""
+    group = layers if isinstance(layers, Q4Group) else Q4Group(layers)
+    B = _q4_batch(x, group.n, group.device)
+    if len(ys) != len(group):
+        raise NQError(NQ_ERR_INVALID_ARG, "one output per layer")
+    for y, L in zip(ys, group.layers):
+        _q4_output(x, B, y, L.m, ys[0].dtype)
+    _q4_scratch(workspace, group.device)
+    yp = (ctypes.c_void_p * len(ys))(*[y.data_ptr() for y in ys])
+    _on_stream(group.device, stream, lambda s: _check(lib().nq_q4_linear_fwd_group(
+        group.ref, len(group), x.data_ptr(), _DT[x.dtype], yp, _DT[ys[0].dtype], B, workspace.data_ptr(),
+        workspace.numel(), s)))
+    return ys
+
+
+def q4_linear_group(x: torch.Tensor, layers, out_dtype: torch.dtype | None = None, stream=None):
+    """[x W_l^T] for 4-bit layers sharing x."""
+    group = layers if isinstance(layers, Q4Group) else Q4Group(layers)
+
+    def call(_):
+        xx = x.contiguous()
+        B = _q4_batch(xx, group.n, group.device)
+        ys = [torch.empty((*xx.shape[:-1], L.m), dtype=out_dtype or x.dtype, device=x.device) for L in group.layers]
+        return q4_linear_group_into(xx, group, ys, new_q4_workspace(group, B))
+
+    return _on_stream(group.device, stream, call)
+
+
+# ------------------------------------------------------------------ block norms
+class BlockNorm:
+    """What stands between the linears of two blocks (nq_block_norm): the norm
+    behind a block with weight w_post (post=False: none), its gate, the residual
+    sum with its scales, and the norm before the next block with weight w_pre
+    (pre=False: none).  Weights and the channel gate are (d,) GPU tensors of one
+    dtype, fp32, fp16 or bf16; a norm without a weight multiplies by 1."""
+
+    def __init__(self, d: int, act_dtype: torch.dtype = torch.bfloat16, res_dtype: torch.dtype | None = None,
+                 w_post: torch.Tensor | None = None, w_pre: torch.Tensor | None = None,
+                 gate: torch.Tensor | None = None, post: bool = True, pre: bool = True, res_scale: float = 1.0,
+                 block_scale: float = 1.0, weight_offset: float = 0.0, eps: float = 1e-5):
+        given = [t for t in (w_post, w_pre, gate) if t is not None]
+        self.d, self.act_dtype, self.res_dtype = d, act_dtype, res_dtype or act_dtype
+        self.w_post, self.w_pre, self.gate, self.post, self.pre = w_post, w_pre, gate, post, pre
+        self.device = given[0].device if given else None
+        dtype = given[0].dtype if given else torch.float32
+        for t, name in ((w_post, "w_post"), (w_pre, "w_pre"), (gate, "gate")):
+            if t is not None:
+                _gpu_tensor(t, name, dtype, (d,), self.device)
+        if given and not given[0].is_cuda:
+            raise NQError(NQ_ERR_INVALID_ARG, "the weights must be GPU tensors")
+        if any(t not in _DT for t in (act_dtype, self.res_dtype, dtype)):
+            raise NQError(NQ_ERR_INVALID_ARG, "dtypes must be fp32, fp16 or bf16")
+        if (w_post is not None and not post) or (w_pre is not None and not pre):
+            raise NQError(NQ_ERR_INVALID_ARG, "a weight for a norm that is left out")
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self.c = nq_block_norm(d, NQ_NORM_POST * bool(post) | NQ_NORM_PRE * bool(pre), _DT[act_dtype],
+                               _DT[self.res_dtype], _DT[dtype], eps, res_scale, block_scale, weight_offset,
+                               ptr(w_post), ptr(w_pre), ptr(gate))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.c)
+
+    def check(self, t, name, dtype, shape, device):
+        if t is not None:
+            _gpu_tensor(t, name, dtype, shape, device)
+            return t.data_ptr()
+        return None
+
+
+def _norm_rows(h: torch.Tensor, norm: BlockNorm):
+    if h.dim() != 2 or not h.is_cuda or (norm.device is not None and h.device != norm.device):
+        raise NQError(NQ_ERR_INVALID_ARG, f"the residual stream must be a (rows, {norm.d}) GPU tensor on the weights' "
+                                          "device")
+    return h.shape[0], torch.Size((h.shape[0], norm.d))
+
+
+def block_norm(h: torch.Tensor, y: torch.Tensor | None, norm: BlockNorm, gate: torch.Tensor | None = None,
+               inplace: bool = False, with_stats: bool = False, stream=None):
+    """(h', x) or, with_stats, (h', x, stats): h' = res_scale h + block_scale gate
+    post(y), x = pre(h') (None for a norm without `pre`).  h (rows, d) is the
+    residual stream, y the block's output, `gate` one gate for each row and
+    channel.  inplace writes h' over h; with y None h' is h.  stats (2, rows) is
+    what block_norm_backward takes."""
+    rows, shape = _norm_rows(h, norm)
+    dev, check = h.device, norm.check
+    hp, yp = check(h, "h", norm.res_dtype, shape, dev), check(y, "y", norm.act_dtype, shape, dev)
+    gp = check(gate, "gate", norm.act_dtype, shape, dev)
+
+    def call(s):
+        h_out = h if inplace or y is None else torch.empty_like(h)
+        x = torch.empty(shape, dtype=norm.act_dtype, device=dev) if norm.pre else None
+        stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if with_stats else None
+        _check(lib().nq_block_norm_fwd(norm.ref, rows, hp, yp, gp, h_out.data_ptr(),
+                                       x.data_ptr() if norm.pre else None, stats.data_ptr() if with_stats else None,
+                                       s))
+        return (h_out, x, stats) if with_stats else (h_out, x)
+
+    return _on_stream(dev, stream, call)
+
+
+def block_norm_backward(dx: torch.Tensor | None, dh: torch.Tensor | None, h: torch.Tensor, y: torch.Tensor | None,
+                        stats: torch.Tensor, norm: BlockNorm, gate: torch.Tensor | None = None,
+                        inplace: bool = False, workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of block_norm from dx and dh, the gradients of x and h' (dh None:
+    zero), with h its h' and y, stats and gate as there.  Returns a dict of "dh"
+    (written over the given dh with inplace), "dy" (with y) and, where the norm
+    has them, "dw_pre", "dw_post" and "dgate" (fp32; for a gate of each row and
+    channel its own dtype)."""
+    rows, shape = _norm_rows(h, norm)
+    dev, check, f32 = h.device, norm.check, torch.float32
+    hp, yp = check(h, "h", norm.res_dtype, shape, dev), check(y, "y", norm.act_dtype, shape, dev)
+    dxp = check(dx, "dx", norm.act_dtype, shape, dev)
+    dhp, gp = check(dh, "dh", norm.res_dtype, shape, dev), check(gate, "gate", norm.act_dtype, shape, dev)
+    sp = check(stats, "stats", f32, (2, rows), dev)
+    if inplace and dh is None:
+        raise NQError(NQ_ERR_INVALID_ARG, "inplace needs dh")
+
+    def call(s):
+        out = {"dh": dh if inplace else torch.empty_like(h)}
+        if norm.w_pre is not None:
+            out["dw_pre"] = torch.empty(norm.d, dtype=f32, device=dev)
+        if y is not None and (gate is not None or norm.gate is not None):
+            out["dgate"] = torch.empty_like(gate) if gate is not None else torch.empty(norm.d, dtype=f32, device=dev)
+        if y is not None and norm.w_post is not None:
+            out["dw_post"] = torch.empty(norm.d, dtype=f32, device=dev)
+        if y is not None:
+            out["dy"] = torch.empty_like(y)
+        ptr = lambda k: out[k].data_ptr() if k in out else None  # noqa: E731
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(int(lib().nq_block_norm_workspace_bytes(norm.ref, rows)), 256), dtype=torch.uint8,
+                             device=dev)
+        rows_gate = gate is not None
+        _check(lib().nq_block_norm_bwd(norm.ref, rows, dxp, dhp, hp, yp, gp, sp, ptr("dh"), ptr("dy"),
+                                       ptr("dgate") if rows_gate else None, ptr("dw_post"), ptr("dw_pre"),
+                                       None if rows_gate else ptr("dgate"), ws.data_ptr(), ws.numel(), s))
+        return out
+
+    return _on_stream(dev, stream, call)
 
 
 def bits_per_weight(m: int, n: int, r: int, scale_bits: int = 16) -> float:

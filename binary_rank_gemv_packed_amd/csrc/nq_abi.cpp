@@ -704,6 +704,349 @@ nq_status nq_balance_scales(float* s1, float* g, float* s2, int32_t m, int32_t n
   return ok();
 }
 
+// ------------------------------------------------------------------ 4-bit linears
+static bool q4_dims_ok(int32_t m, int32_t n, int32_t group, int32_t scale_dtype, int32_t zeros) {
+  return m >= 1 && m <= MAX_DIM && n >= 1 && n <= MAX_DIM && (group == 32 || group == 64 || group == 128) &&
+         scale_bytes(scale_dtype) && (zeros == 0 || zeros == 1);
+}
+
+static nq::Q4Layout q4_layout_of(const nq_q4_layer* L) {
+  return nq::q4_layout(L->m, L->n, L->group, scale_bytes(L->scale_dtype), L->zeros != 0);
+}
+
+static nq_status check_q4(const nq_q4_layer* L) {
+  if (!L) return fail(NQ_ERR_INVALID_ARG, "layer is NULL");
+  if (!q4_dims_ok(L->m, L->n, L->group, L->scale_dtype, L->zeros))
+    return fail(NQ_ERR_INVALID_ARG,
+                "4-bit layer m=%d n=%d (1..%d) group=%d (32, 64 or 128) scale_dtype=%d (NQ_F16 or NQ_F32) zeros=%d (0 "
+                "or 1)",
+                L->m, L->n, MAX_DIM, L->group, L->scale_dtype, L->zeros);
+  if (!L->blob) return fail(NQ_ERR_INVALID_ARG, "layer blob is NULL");
+  if (reinterpret_cast<uintptr_t>(L->blob) % 256) return fail(NQ_ERR_INVALID_ARG, "layer blob is not 256-byte aligned");
+  return NQ_OK;
+}
+
+size_t nq_q4_layer_bytes(int32_t m, int32_t n, int32_t group, int32_t scale_dtype, int32_t zeros) {
+  if (!q4_dims_ok(m, n, group, scale_dtype, zeros)) return 0;
+  return nq::q4_layout(m, n, group, scale_bytes(scale_dtype), zeros != 0).total;
+}
+
+nq_status nq_q4_pack(const nq_q4_layer* L, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                     nq_stream_t stream) {
+  nq_status st = check_q4(L);
+  if (st) return st;
+  if (!codes || !scales) return fail(NQ_ERR_INVALID_ARG, "codes and scales must be non-NULL");
+  if ((zeros != nullptr) != (L->zeros != 0))
+    return fail(NQ_ERR_INVALID_ARG, L->zeros ? "zeros is NULL" : "zeros given for a layer without zero points");
+  const int sb = scale_bytes(L->scale_dtype);
+  if (reinterpret_cast<uintptr_t>(scales) % sb)
+    return fail(NQ_ERR_INVALID_ARG, "scales is not aligned to its element size");
+  const nq::Q4Layout lay = q4_layout_of(L);
+  const size_t groups = (size_t)L->m * nq::ceil_div(L->n, L->group);
+  if (spans_overlap(L->blob, lay.total, codes, (size_t)L->m * L->n) ||
+      spans_overlap(L->blob, lay.total, scales, groups * sb) || (zeros && spans_overlap(L->blob, lay.total, zeros, groups)))
+    return fail(NQ_ERR_INVALID_ARG, "the blob and an input overlap");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  uint8_t* blob = static_cast<uint8_t*>(L->blob);
+  nq::Q4Header h;
+  memset(&h, 0, sizeof(h));
+  h.magic = nq::Q4_MAGIC;
+  h.version = nq::Q4_VERSION;
+  h.m = L->m;
+  h.n = L->n;
+  h.group = L->group;
+  h.scale_dtype = L->scale_dtype;
+  h.zeros = L->zeros;
+  h.off_codes = lay.off_codes;
+  h.off_scales = lay.off_scales;
+  h.off_zeros = lay.off_zeros;
+  h.total = lay.total;
+  (void)hipGetLastError();
+  hipError_t e = hipMemcpyAsync(blob, &h, sizeof(h), hipMemcpyHostToDevice, s);
+  if (e != hipSuccess) return hip_fail(e, "header copy");
+  int* bad = reinterpret_cast<int*>(blob + offsetof(nq::Q4Header, bad));
+  e = nq::q4_pack(lay, L->m, L->n, L->group, sb, codes, scales, zeros, blob, bad, s);
+  if (e != hipSuccess) return hip_fail(e, "4-bit pack launch");
+  int bad_host = 0;
+  e = hipMemcpyAsync(&bad_host, bad, sizeof(int), hipMemcpyDeviceToHost, s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return hip_fail(e, "4-bit pack synchronise");
+  if (bad_host) return fail(NQ_ERR_RANGE, "a code or zero point is above 15");
+  return ok();
+}
+
+nq_status nq_q4_unpack(const nq_q4_layer* L, uint8_t* codes, uint8_t* zeros, nq_stream_t stream) {
+  nq_status st = check_q4(L);
+  if (st) return st;
+  if (!codes) return fail(NQ_ERR_INVALID_ARG, "codes must be non-NULL");
+  if (zeros && !L->zeros) return fail(NQ_ERR_INVALID_ARG, "zeros asked of a layer without zero points");
+  const nq::Q4Layout lay = q4_layout_of(L);
+  const size_t groups = (size_t)L->m * nq::ceil_div(L->n, L->group);
+  if (spans_overlap(L->blob, lay.total, codes, (size_t)L->m * L->n) ||
+      (zeros && spans_overlap(L->blob, lay.total, zeros, groups)))
+    return fail(NQ_ERR_INVALID_ARG, "the blob and an output overlap");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  hipError_t e = nq::q4_unpack(lay, L->m, L->n, L->group, static_cast<const uint8_t*>(L->blob), codes, zeros, s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return hip_fail(e, "4-bit unpack");
+  return ok();
+}
+
+static nq_status check_q4_group(const nq_q4_layer* const* layers, int32_t L) {
+  if (!layers || L < 1 || L > NQ_GROUP_MAX)
+    return fail(NQ_ERR_INVALID_ARG, "a group holds 1..%d layers (got %d)", NQ_GROUP_MAX, L);
+  for (int32_t l = 0; l < L; l++) {
+    const nq_status st = check_q4(layers[l]);
+    if (st) return st;
+    const nq_q4_layer &a = *layers[0], &b = *layers[l];
+    if (b.n != a.n || b.group != a.group || b.scale_dtype != a.scale_dtype || b.zeros != a.zeros)
+      return fail(NQ_ERR_INVALID_ARG, "layer %d of a group that shares x differs in n, group, scale dtype or zeros", l);
+  }
+  return NQ_OK;
+}
+
+size_t nq_q4_workspace_bytes_group(const nq_q4_layer* const* layers, int32_t L, int32_t B) {
+  if (check_q4_group(layers, L) || B <= 0 || B > MAX_BATCH) return 0;
+  int m[NQ_GROUP_MAX];
+  for (int32_t l = 0; l < L; l++) m[l] = layers[l]->m;
+  return nq::q4_workspace(m, L, layers[0]->n, B, NQ_F32);  // fp32 x needs the most
+}
+
+size_t nq_q4_workspace_bytes(const nq_q4_layer* L, int32_t B) { return nq_q4_workspace_bytes_group(&L, 1, B); }
+
+nq_status nq_q4_linear_fwd_group(const nq_q4_layer* const* layers, int32_t L, const void* x, int32_t x_dtype,
+                                 void* const* ys, int32_t y_dtype, int32_t B, void* workspace,
+                                 size_t workspace_bytes, nq_stream_t stream) {
+  nq_status st = check_q4_group(layers, L);
+  if (st) return st;
+  if (B < 0 || B > MAX_BATCH) return fail(NQ_ERR_INVALID_ARG, "batch %d out of range 0..%d", B, MAX_BATCH);
+  const int xb = act_bytes(x_dtype), yb = act_bytes(y_dtype);
+  if (!xb) return fail(NQ_ERR_INVALID_ARG, "x_dtype %d is not NQ_BF16 or NQ_F32", x_dtype);
+  if (!yb) return fail(NQ_ERR_INVALID_ARG, "y_dtype %d is not NQ_BF16 or NQ_F32", y_dtype);
+  if (B == 0) return ok();
+  if (!x || !ys) return fail(NQ_ERR_INVALID_ARG, "x and y must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(x) % xb) return fail(NQ_ERR_INVALID_ARG, "x is not aligned to its element size");
+  nq::Q4Args a{};
+  a.L = L;
+  a.n = layers[0]->n;
+  a.B = B;
+  a.group = layers[0]->group;
+  a.scale_dtype = layers[0]->scale_dtype;
+  a.zeros = layers[0]->zeros != 0;
+  a.x_dtype = x_dtype;
+  a.y_dtype = y_dtype;
+  a.x = x;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.stream = reinterpret_cast<hipStream_t>(stream);
+  const size_t x_bytes = (size_t)B * a.n * xb;
+  for (int32_t l = 0; l < L; l++) {
+    a.m[l] = layers[l]->m;
+    a.blob[l] = static_cast<const uint8_t*>(layers[l]->blob);
+    a.y[l] = ys[l];
+  }
+  const size_t need = nq::q4_workspace(a.m, L, a.n, B, x_dtype);
+  for (int32_t l = 0; l < L; l++) {
+    if (!ys[l]) return fail(NQ_ERR_INVALID_ARG, "x and y must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(ys[l]) % yb) return fail(NQ_ERR_INVALID_ARG, "y is not aligned to its element size");
+    const size_t y_bytes = (size_t)B * a.m[l] * yb;
+    if (spans_overlap(x, x_bytes, ys[l], y_bytes)) return fail(NQ_ERR_INVALID_ARG, "x and y overlap");
+    if (need && workspace && spans_overlap(workspace, need, ys[l], y_bytes))
+      return fail(NQ_ERR_INVALID_ARG, "y and the workspace overlap");
+    for (int32_t k = 0; k < l; k++)
+      if (spans_overlap(ys[k], (size_t)B * a.m[k] * yb, ys[l], y_bytes))
+        return fail(NQ_ERR_INVALID_ARG, "outputs %d and %d overlap", k, l);
+  }
+  if (workspace_bytes < need)
+    return fail(NQ_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);
+  if (need && !workspace) return fail(NQ_ERR_INVALID_ARG, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(NQ_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  if (need && spans_overlap(workspace, need, x, x_bytes))
+    return fail(NQ_ERR_INVALID_ARG, "x and the workspace overlap");
+  (void)hipGetLastError();
+  const hipError_t e = nq::q4_forward(a);
+  if (e != hipSuccess) return hip_fail(e, "4-bit forward launch");
+  return ok();
+}
+
+nq_status nq_q4_linear_fwd(const nq_q4_layer* L, const void* x, int32_t x_dtype, void* y, int32_t y_dtype, int32_t B,
+                           void* workspace, size_t workspace_bytes, nq_stream_t stream) {
+  return nq_q4_linear_fwd_group(&L, 1, x, x_dtype, &y, y_dtype, B, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ block norms
+namespace {
+
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+int any_bytes(int32_t dt) { return dt == NQ_F32 ? 4 : (dt == NQ_F16 || dt == NQ_BF16 ? 2 : 0); }
+
+nq_status check_norm(const nq_block_norm* N, int32_t rows) {
+  if (!N) return fail(NQ_ERR_INVALID_ARG, "norm is NULL");
+  if (N->d < 1 || N->d > NQ_NORM_MAX_DIM)
+    return fail(NQ_ERR_INVALID_ARG, "d=%d out of range 1..%d", N->d, NQ_NORM_MAX_DIM);
+  if (rows < 0 || rows > MAX_BATCH) return fail(NQ_ERR_INVALID_ARG, "rows %d out of range 0..%d", rows, MAX_BATCH);
+  if (N->flags & ~(NQ_NORM_POST | NQ_NORM_PRE)) return fail(NQ_ERR_INVALID_ARG, "unknown flags %d", N->flags);
+  if (!act_bytes(N->act_dtype)) return fail(NQ_ERR_INVALID_ARG, "act_dtype %d is not NQ_BF16 or NQ_F32", N->act_dtype);
+  if (N->res_dtype != NQ_F32 && N->res_dtype != N->act_dtype)
+    return fail(NQ_ERR_INVALID_ARG, "res_dtype %d is neither NQ_F32 nor act_dtype", N->res_dtype);
+  const int pb = any_bytes(N->param_dtype);
+  if (!pb) return fail(NQ_ERR_INVALID_ARG, "param_dtype %d is not NQ_F32, NQ_F16 or NQ_BF16", N->param_dtype);
+  if (!(N->eps > 0.0f) || !std::isfinite(N->eps)) return fail(NQ_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!std::isfinite(N->res_scale) || !std::isfinite(N->block_scale) || !std::isfinite(N->weight_offset))
+    return fail(NQ_ERR_INVALID_ARG, "res_scale, block_scale and weight_offset must be finite");
+  if (reinterpret_cast<uintptr_t>(N->w_post) % pb || reinterpret_cast<uintptr_t>(N->w_pre) % pb ||
+      reinterpret_cast<uintptr_t>(N->gate) % pb)
+    return fail(NQ_ERR_INVALID_ARG, "w_post, w_pre or gate is not aligned to its element size");
+  return NQ_OK;
+}
+
+// Every output apart from every input and from the other outputs; outs[inplace]
+// may be ins[inplace] itself.
+nq_status check_apart(const Span* outs, int no, const Span* ins, int ni, int inplace) {
+  for (int i = 0; i < no; i++) {
+    if (!outs[i].p) continue;
+    for (int k = 0; k < ni; k++) {
+      if (!ins[k].p || (i == inplace && k == inplace && outs[i].p == ins[k].p)) continue;
+      if (spans_overlap(outs[i].p, outs[i].bytes, ins[k].p, ins[k].bytes))
+        return fail(NQ_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, ins[k].name);
+    }
+    for (int k = 0; k < i; k++)
+      if (outs[k].p && spans_overlap(outs[i].p, outs[i].bytes, outs[k].p, outs[k].bytes))
+        return fail(NQ_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, outs[k].name);
+  }
+  return NQ_OK;
+}
+
+nq::NormArgs norm_args(const nq_block_norm* N, int32_t rows, nq_stream_t stream) {
+  nq::NormArgs a{};
+  a.rows = rows;
+  a.d = N->d;
+  a.act_dtype = N->act_dtype;
+  a.res_dtype = N->res_dtype;
+  a.param_dtype = N->param_dtype;
+  a.post = (N->flags & NQ_NORM_POST) != 0;
+  a.pre = (N->flags & NQ_NORM_PRE) != 0;
+  a.eps = N->eps;
+  a.res_scale = N->res_scale;
+  a.block_scale = N->block_scale;
+  a.weight_offset = N->weight_offset;
+  a.w_post = N->w_post;
+  a.w_pre = N->w_pre;
+  a.gate = N->gate;
+  a.stream = reinterpret_cast<hipStream_t>(stream);
+  return a;
+}
+
+bool misaligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+}  // namespace
+
+nq_status nq_block_norm_fwd(const nq_block_norm* N, int32_t rows, const void* h, const void* y, const void* gate_rows,
+                            void* h_out, void* x, float* stats, nq_stream_t stream) {
+  nq_status st = check_norm(N, rows);
+  if (st) return st;
+  const bool pre = N->flags & NQ_NORM_PRE;
+  if (rows == 0) return ok();
+  if (!h || (y && !h_out) || (pre && !x)) return fail(NQ_ERR_INVALID_ARG, "h, h_out (with y) and x (with NQ_NORM_PRE) must be non-NULL");
+  if (!y && !pre) return fail(NQ_ERR_INVALID_ARG, "nothing to do: neither y nor NQ_NORM_PRE");
+  if (gate_rows && (N->gate || !y))
+    return fail(NQ_ERR_INVALID_ARG, N->gate ? "gate_rows together with a channel gate" : "gate_rows without y");
+  const int ab = act_bytes(N->act_dtype), rb = act_bytes(N->res_dtype), pb = any_bytes(N->param_dtype);
+  if (misaligned(h, rb) || misaligned(h_out, rb) || misaligned(y, ab) || misaligned(x, ab) ||
+      misaligned(gate_rows, ab) || misaligned(stats, 4))
+    return fail(NQ_ERR_INVALID_ARG, "a tensor is not aligned to its element size");
+  nq::NormArgs a = norm_args(N, rows, stream);
+  a.h = h;
+  a.y = y;
+  a.gate_rows = gate_rows;
+  a.h_out = y ? h_out : nullptr;
+  a.x = pre ? x : nullptr;
+  a.stats = stats;
+  const size_t count = (size_t)rows * N->d, w = (size_t)N->d * pb;
+  const Span outs[] = {{a.h_out, count * rb, "h_out"}, {a.x, count * ab, "x"}, {stats, (size_t)rows * 8, "stats"}};
+  const Span ins[] = {{h, count * rb, "h"},     {y, count * ab, "y"},          {gate_rows, count * ab, "gate_rows"},
+                      {N->w_post, w, "w_post"}, {N->w_pre, w, "w_pre"},        {N->gate, w, "gate"}};
+  st = check_apart(outs, 3, ins, 6, 0);
+  if (st) return st;
+  (void)hipGetLastError();
+  const hipError_t e = nq::norm_forward(a);
+  if (e != hipSuccess) return hip_fail(e, "block norm launch");
+  return ok();
+}
+
+size_t nq_block_norm_workspace_bytes(const nq_block_norm* N, int32_t rows) {
+  if (check_norm(N, rows)) return 0;
+  return nq::align_up((size_t)nq::norm_bwd_parts(rows) * 2 * N->d * 4, 256);
+}
+
+nq_status nq_block_norm_bwd(const nq_block_norm* N, int32_t rows, const void* dx, const void* dh_out,
+                            const void* h_out, const void* y, const void* gate_rows, const float* stats, void* dh,
+                            void* dy, void* dgate_rows, float* dw_post, float* dw_pre, float* dgate, void* workspace,
+                            size_t workspace_bytes, nq_stream_t stream) {
+  nq_status st = check_norm(N, rows);
+  if (st) return st;
+  const bool pre = N->flags & NQ_NORM_PRE, post = N->flags & NQ_NORM_POST;
+  const int ab = act_bytes(N->act_dtype), rb = act_bytes(N->res_dtype), pb = any_bytes(N->param_dtype);
+  if (rows) {
+    if (!y && !pre) return fail(NQ_ERR_INVALID_ARG, "nothing to do: neither y nor NQ_NORM_PRE");
+    if (!dh || (y && !dy) || (pre && (!dx || !h_out)) || ((pre || (post && y)) && !stats))
+      return fail(NQ_ERR_INVALID_ARG,
+                  "dh, dy (with y), dx and h_out (with NQ_NORM_PRE) and stats (with a norm) must be non-NULL");
+    if (gate_rows && (N->gate || !y))
+      return fail(NQ_ERR_INVALID_ARG, N->gate ? "gate_rows together with a channel gate" : "gate_rows without y");
+    if ((gate_rows != nullptr) != (dgate_rows != nullptr))
+      return fail(NQ_ERR_INVALID_ARG, "gate_rows and dgate_rows must be given together");
+    if ((dw_post || dgate) && !y) return fail(NQ_ERR_INVALID_ARG, "dw_post or dgate without y");
+  }
+  if ((dw_post && !(post && N->w_post)) || (dw_pre && !(pre && N->w_pre)) || (dgate && !N->gate))
+    return fail(NQ_ERR_INVALID_ARG, "dw_post, dw_pre or dgate asked for without its w_post, w_pre or gate");
+  const bool sums = dw_post || dw_pre || dgate;
+  if (!rows && !sums) return ok();
+  if (misaligned(dx, ab) || misaligned(dh_out, rb) || misaligned(h_out, rb) || misaligned(y, ab) ||
+      misaligned(gate_rows, ab) || misaligned(stats, 4) || misaligned(dh, rb) || misaligned(dy, ab) ||
+      misaligned(dgate_rows, ab) || misaligned(dw_post, 4) || misaligned(dw_pre, 4) || misaligned(dgate, 4))
+    return fail(NQ_ERR_INVALID_ARG, "a tensor is not aligned to its element size");
+  const size_t need = sums ? nq_block_norm_workspace_bytes(N, rows) : 0;
+  if (workspace_bytes < need)
+    return fail(NQ_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);
+  if (need && !workspace) return fail(NQ_ERR_INVALID_ARG, "workspace is NULL");
+  if (misaligned(workspace, 256)) return fail(NQ_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  nq::NormArgs a = norm_args(N, rows, stream);
+  a.dx = pre ? dx : nullptr;
+  a.dh_out = dh_out;
+  a.h = pre ? h_out : nullptr;
+  a.y = y;
+  a.gate_rows = gate_rows;
+  a.stats = const_cast<float*>(stats);
+  a.dh = dh;
+  a.dy = y ? dy : nullptr;
+  a.dgate_rows = dgate_rows;
+  a.dw_post = dw_post;
+  a.dw_pre = dw_pre;
+  a.dgate = dgate;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  const size_t count = (size_t)rows * N->d, w = (size_t)N->d * pb, s = (size_t)N->d * 4;
+  const Span outs[] = {{dh, count * rb, "dh"},      {a.dy, count * ab, "dy"}, {dgate_rows, count * ab, "dgate_rows"},
+                       {dw_post, s, "dw_post"},     {dw_pre, s, "dw_pre"},    {dgate, s, "dgate"},
+                       {need ? workspace : nullptr, need, "the workspace"}};
+  const Span ins[] = {{dh_out, count * rb, "dh_out"}, {a.dx, count * ab, "dx"},
+                      {a.h, count * rb, "h_out"},     {y, count * ab, "y"},
+                      {gate_rows, count * ab, "gate_rows"}, {stats, (size_t)rows * 8, "stats"},
+                      {N->w_post, w, "w_post"},       {N->w_pre, w, "w_pre"},
+                      {N->gate, w, "gate"}};
+  st = check_apart(outs, 7, ins, 9, 0);
+  if (st) return st;
+  (void)hipGetLastError();
+  const hipError_t e = nq::norm_backward(a);
+  if (e != hipSuccess) return hip_fail(e, "block norm backward launch");
+  return ok();
+}
+
 double nq_bits_per_weight(int32_t m, int32_t n, int32_t r, int32_t scale_bits) {
   if (m < 1 || n < 1 || r < 0 || scale_bits < 0) return -1.0;
   return ((double)r * ((double)m + n) + (double)scale_bits * ((double)m + n + r)) / ((double)m * n);
@@ -729,6 +1072,7 @@ const char* nq_status_string(int32_t s) {
     case NQ_ERR_UNSUPPORTED: return "unsupported by the chosen path";
     case NQ_ERR_HIP: return "HIP runtime error";
     case NQ_ERR_INTERNAL: return "internal error";
+    case NQ_ERR_RANGE: return "4-bit code or zero point above 15";
   }
   return "unknown status";
 }

@@ -162,6 +162,41 @@ __host__ __device__ inline float plane_factor(int k) {
 }
 
 // ---------------------------------------------------------------------------
+// 4-bit layers (nq_q4.hip).  A weight of m rows and n columns is stored as tiles
+// of 16 rows x 128 columns, row tiles slowest; a tile is 64 lanes x 16 bytes, one
+// wavefront's load and its fp16 operands of four 16x16x32 MFMAs:
+//   lane L, word t holds row 16*rt + (L & 15), columns 128*kt + 32*t + 8*(L >> 4) + [0, 8);
+//   nibble p of the word is column 2p of the eight, nibble p + 4 column 2p + 1 (p < 4).
+// Codes of rows >= m or columns >= n are 0.  Scales and zero points (one byte)
+// are stored as [row tile][column tile][group of the tile][16 rows], 128 / G
+// groups a tile; entries that belong to no group are 0.
+// Blob: header | codes | scales | zero points (if any), each 256-byte aligned.
+// ---------------------------------------------------------------------------
+constexpr uint32_t Q4_MAGIC = 0x3134514eu;  // "NQ41"
+constexpr uint32_t Q4_VERSION = 1;
+
+struct Q4Header {
+  uint32_t magic, version;
+  int32_t m, n, group, scale_dtype, zeros;
+  int32_t bad;  // set by the pack kernels when a code or zero point is above 15
+  uint64_t off_codes, off_scales, off_zeros, total;
+};
+
+struct Q4Layout {
+  size_t off_codes, off_scales, off_zeros, total;
+};
+
+__host__ __device__ inline Q4Layout q4_layout(int m, int n, int group, int scale_bytes, bool zeros) {
+  const size_t tiles = (size_t)ceil_div(m, 16) * ceil_div(n, 128), entries = tiles * (128 / group) * 16;
+  Q4Layout l;
+  l.off_codes = HEADER_BYTES;
+  l.off_scales = align_up(l.off_codes + tiles * 1024, 256);
+  l.off_zeros = align_up(l.off_scales + entries * scale_bytes, 256);
+  l.total = align_up(l.off_zeros + (zeros ? entries : 0), 256);
+  return l;
+}
+
+// ---------------------------------------------------------------------------
 // Device helpers
 // ---------------------------------------------------------------------------
 __device__ inline int floor_log2(float a) {  // a > 0, finite

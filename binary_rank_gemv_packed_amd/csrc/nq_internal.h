@@ -172,5 +172,65 @@ size_t admm_workspace_bytes(int m, int n, int r);
 hipError_t admm_run(const AdmmArgs& a);
 hipError_t launch_balance(float* s1, float* g, float* s2, int m, int n, int r, hipStream_t st);
 
-}  // namespace nq
+// Linears with 4-bit weights (nq_q4.hip): L <= GROUP_MAX layers of one width,
+// group, scale type and kind of zero point that read the same x.
+constexpr int Q4_DEC_MAX = 64;  // rows of x that run on the decode kernel, 16 at a time
+struct Q4Args {
+  int L, n, B;
+  int m[GROUP_MAX];
+  int group, scale_dtype;
+  bool zeros;
+  int x_dtype, y_dtype;
+  const uint8_t* blob[GROUP_MAX];
+  const void* x;
+  void* y[GROUP_MAX];
+  uint8_t* ws;
+  hipStream_t stream;
+};
+struct Q4GemmPlan {
+  int S;  // K splits
+  size_t off_hi, off_lo, off_fac, off_part, bytes;
+};
+struct Q4Layout;
+Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype);
+size_t q4_workspace(const int* m, int L, int n, int B, int x_dtype);
+hipError_t q4_forward(const Q4Args& a);
+hipError_t q4_pack(const Q4Layout& lay, int m, int n, int group, int scale_bytes, const uint8_t* q, const void* s,
+                   const uint8_t* z, uint8_t* blob, int* bad, hipStream_t st);
+hipError_t q4_unpack(const Q4Layout& lay, int m, int n, int group, const uint8_t* blob, uint8_t* q, uint8_t* z,
+                     hipStream_t st);
 
+// Norms between two blocks (nq_norm.hip).  Forward: h, y, gate_rows -> h_out, x,
+// stats; backward: dx, dh_out, h (= h_out of the forward), y, gate_rows, stats ->
+// dh, dy, dgate_rows and, through part, dw_post, dw_pre, dgate.
+constexpr int NORM_MAX_DIM = 32768;  // 1024 threads x 32 columns
+struct NormArgs {
+  int rows, d;
+  int act_dtype, res_dtype, param_dtype;
+  bool post, pre;
+  float eps, res_scale, block_scale, weight_offset;
+  const void* w_post;
+  const void* w_pre;
+  const void* gate;
+  const void* gate_rows;
+  const void* h;
+  const void* y;
+  void* h_out;
+  void* x;
+  float* stats;
+  const void* dx;
+  const void* dh_out;
+  void* dh;
+  void* dy;
+  void* dgate_rows;
+  float* dw_post;
+  float* dw_pre;
+  float* dgate;
+  float* part;  // [norm_bwd_parts(rows)][2][d], null when no sum over rows is asked for
+  hipStream_t stream;
+};
+int norm_bwd_parts(int rows);
+hipError_t norm_forward(const NormArgs& a);
+hipError_t norm_backward(const NormArgs& a);
+
+}  // namespace nq

@@ -1,6 +1,8 @@
 /*
  * nq.h -- C ABI of libnq: linear layers whose weight is a low-rank product of
- * bit-packed sign matrices and diagonal scales, on AMD Instinct MI355X (gfx950).
+ * bit-packed sign matrices and diagonal scales, on AMD Instinct MI355X (gfx950),
+ * and what a model calls beside them: linears with 4-bit weights, and the norms
+ * between its blocks.
  *
  * The operation (hardwired.dev NanoQuant article, section "Jak NanoQuant
  * funguje": the weight is factored into sign matrices and diagonal scales;
@@ -44,7 +46,8 @@ typedef enum {
   NQ_ERR_WORKSPACE = -3,   /* workspace smaller than nq_workspace_bytes()                         */
   NQ_ERR_UNSUPPORTED = -4, /* valid arguments that the chosen path does not handle                */
   NQ_ERR_HIP = -5,         /* a HIP runtime call or launch failed; see nq_last_error()           */
-  NQ_ERR_INTERNAL = -6
+  NQ_ERR_INTERNAL = -6,
+  NQ_ERR_RANGE = -7        /* a 4-bit code or zero point is above 15 (nq_q4_pack only)            */
 } nq_status;
 
 typedef enum { NQ_F32 = 0, NQ_F16 = 1, NQ_BF16 = 2 } nq_dtype;
@@ -252,6 +255,127 @@ nq_status nq_admm_factorize(const float* W, int32_t m, int32_t n, int32_t r, con
  * W_hat is unchanged bit for bit.  NQ_ERR_INVALID_ARG for null pointers or
  * dimensions out of range.  Asynchronous on `stream`. */
 nq_status nq_balance_scales(float* s1, float* g, float* s2, int32_t m, int32_t n, int32_t r, nq_stream_t stream);
+
+/* ------------------------------------------------------------------ 4-bit linears
+ * A linear layer whose weight has 4-bit codes and one scale for each row and
+ * `group` consecutive columns, for the linears that a model keeps at 4 bits
+ * (the INT4 side of the rapidrecap.app recap's comparison, section "Key
+ * Points"):
+ *
+ *     W[i,j] = s[i, j / group] (q[i,j] - z[i, j / group])        (m x n)
+ *     y[b,:] = W . x[b,:]
+ *
+ * `blob` is device memory of nq_q4_layer_bytes() bytes, 256-byte aligned, owned
+ * by the caller, written by nq_q4_pack and position independent.  The last
+ * group of a row may be shorter than the others. */
+typedef struct {
+  int32_t m, n;        /* 1 <= m, n <= 2^20                                             */
+  int32_t group;       /* columns that share a scale: 32, 64 or 128                     */
+  int32_t scale_dtype; /* nq_dtype of the scales: NQ_F16 or NQ_F32                      */
+  int32_t zeros;       /* 1: a zero point for each scale; 0: 8 is the zero point of all */
+  void* blob;          /* device pointer                                                */
+} nq_q4_layer;
+
+/* Bytes of device memory a packed 4-bit layer occupies; 0 for invalid arguments. */
+size_t nq_q4_layer_bytes(int32_t m, int32_t n, int32_t group, int32_t scale_dtype, int32_t zeros);
+
+/* Packs codes, scales and zero points into L->blob.
+ *   codes  : device, m x n uint8 row-major, every code in 0..15
+ *   scales : device, m x ceil(n / group) row-major (L->scale_dtype)
+ *   zeros  : device, m x ceil(n / group) uint8 row-major in 0..15 if L->zeros, else NULL
+ * NQ_ERR_RANGE when a code or zero point is above 15 (the blob is then
+ * unusable).  BLOCKING on `stream`; the inputs may be freed afterwards. */
+nq_status nq_q4_pack(const nq_q4_layer* L, const uint8_t* codes, const void* scales, const uint8_t* zeros,
+                     nq_stream_t stream);
+
+/* Writes the codes (m x n) and, if the layer has them, the zero points back as
+ * nq_q4_pack took them (zeros may be NULL).  Test hook.  BLOCKING on `stream`. */
+nq_status nq_q4_unpack(const nq_q4_layer* L, uint8_t* codes, uint8_t* zeros, nq_stream_t stream);
+
+/* Bytes of device workspace the forward needs for batch B (0 for batches that
+ * run without one, and for invalid arguments).  No initial contents. */
+size_t nq_q4_workspace_bytes(const nq_q4_layer* L, int32_t B);
+
+/* y = x W^T for a batch of B rows, any B.
+ *   x : device, B x n row-major, x_dtype NQ_BF16 or NQ_F32, aligned to its element size
+ *   y : device, B x m row-major, y_dtype NQ_BF16 or NQ_F32, aligned to its element
+ *       size; must not overlap x or the workspace
+ *   workspace : device, >= nq_q4_workspace_bytes(L, B), 256-byte aligned; may be
+ *       NULL when that is 0
+ * The products are exact or off by at most 2^-22, sums are fp32, y is rounded
+ * once.  (Within a row of x, for B up to 64 within 128 columns of it, parts
+ * under 2^-39 of the largest finite value are dropped.)  An infinity or NaN in
+ * a row of x makes every output of that row an infinity or NaN and leaves the
+ * other rows alone.  ASYNCHRONOUS and re-entrant like nq_linear_fwd; may be
+ * captured into a HIP graph; calls that overlap in time need workspaces of their
+ * own.  Repeated calls give identical bits.  B == 0 launches nothing. */
+nq_status nq_q4_linear_fwd(const nq_q4_layer* L, const void* x, int32_t x_dtype, void* y, int32_t y_dtype, int32_t B,
+                           void* workspace, size_t workspace_bytes, nq_stream_t stream);
+
+/* 1..NQ_GROUP_MAX 4-bit layers that read the same x (q, k and v; gate and up):
+ * ys[l] = x W_l^T, B x m_l.  The layers share n, group, scale dtype and kind of
+ * zero point (else NQ_ERR_INVALID_ARG); up to B = 16 one launch runs them all.
+ * No ys[l] may overlap x, the workspace or another. */
+size_t nq_q4_workspace_bytes_group(const nq_q4_layer* const* layers, int32_t L, int32_t B);
+nq_status nq_q4_linear_fwd_group(const nq_q4_layer* const* layers, int32_t L, const void* x, int32_t x_dtype,
+                                 void* const* ys, int32_t y_dtype, int32_t B, void* workspace,
+                                 size_t workspace_bytes, nq_stream_t stream);
+
+/* ------------------------------------------------------------------ block norms
+ * What stands between the linears of two blocks: the norm behind one block, its
+ * gate, the residual sum and the norm before the next, in one launch.  For each
+ * of `rows` rows of d values:
+ *
+ *     u  = y ry (w_post + weight_offset),  ry = (mean y^2 + eps)^-1/2   (without NQ_NORM_POST: u = y)
+ *     h' = res_scale h + block_scale gate u                             (without a gate: gate = 1)
+ *     x  = h' rh (w_pre + weight_offset),  rh = (mean h'^2 + eps)^-1/2  (without NQ_NORM_PRE: no x)
+ *
+ * h is the residual stream, y the block's output (both rows x d row-major), x
+ * the next block's input.  With y NULL h' = h: the norm before the first block. */
+#define NQ_NORM_POST 1
+#define NQ_NORM_PRE 2
+#define NQ_NORM_MAX_DIM 32768
+typedef struct {
+  int32_t d;                  /* 1 <= d <= NQ_NORM_MAX_DIM                                        */
+  int32_t flags;              /* NQ_NORM_POST | NQ_NORM_PRE, one of them at least or y given      */
+  int32_t act_dtype;          /* of y, x, gate_rows and their gradients: NQ_BF16 or NQ_F32        */
+  int32_t res_dtype;          /* of h, h' and their gradients: act_dtype or NQ_F32                */
+  int32_t param_dtype;        /* of w_post, w_pre and gate: NQ_F32, NQ_F16 or NQ_BF16             */
+  float eps;                  /* > 0                                                              */
+  float res_scale, block_scale, weight_offset; /* finite                                          */
+  const void* w_post;         /* device, d values; NULL: 1 and no offset                          */
+  const void* w_pre;          /* device, d values; NULL: 1 and no offset                          */
+  const void* gate;           /* device, d values: one gate for each channel; NULL: none          */
+} nq_block_norm;
+
+/* Forward.  gate_rows (rows x d, act_dtype) is one gate for each row and channel,
+ * NULL for none; not together with N->gate.  h_out may be h itself (the stream is
+ * then updated in place); it is not written (and may be NULL) without y.  x may
+ * be NULL without NQ_NORM_PRE.  stats (2 x rows fp32, may be NULL) receives ry and
+ * rh for the backward pass; the row of a norm that is left out is not written.
+ * Otherwise no output may overlap an input or another output.  All arithmetic is
+ * fp32, every output is rounded once; a row whose sum of squares passes 3.4e38
+ * gives zeros.  Asynchronous on `stream`, no workspace; rows == 0 launches
+ * nothing. */
+nq_status nq_block_norm_fwd(const nq_block_norm* N, int32_t rows, const void* h, const void* y, const void* gate_rows,
+                            void* h_out, void* x, float* stats, nq_stream_t stream);
+
+/* Backward: dx and dh_out are the gradients of x and of h' (dh_out may be NULL
+ * for zero; dx may be NULL without NQ_NORM_PRE), h_out, y, gate_rows and stats are
+ * the forward's (h itself for h_out without y).  Writes dh (res_dtype; may be
+ * dh_out itself), and with y dy (act_dtype) and, with gate_rows, dgate_rows
+ * (act_dtype).  dw_post, dw_pre and dgate (d fp32 each, may be NULL) receive the
+ * sums over all rows, zeros for rows == 0; each needs its N->w_post (and y),
+ * N->w_pre or N->gate (and y).  The workspace holds the workgroups' sums (needed
+ * for these three only, may be NULL without them); no initial contents.  Sums
+ * are added in a fixed order: repeated calls give identical bits.  Asynchronous
+ * on `stream`, capturable; calls that overlap in time need workspaces of their
+ * own. */
+size_t nq_block_norm_workspace_bytes(const nq_block_norm* N, int32_t rows);
+nq_status nq_block_norm_bwd(const nq_block_norm* N, int32_t rows, const void* dx, const void* dh_out,
+                            const void* h_out, const void* y, const void* gate_rows, const float* stats, void* dh,
+                            void* dy, void* dgate_rows, float* dw_post, float* dw_pre, float* dgate, void* workspace,
+                            size_t workspace_bytes, nq_stream_t stream);
 
 /* Average bits per original weight: (r(m+n) + scale_bits (m+n+r)) / (m n)
  * (hardwired.dev, sections "Jak NanoQuant funguje" and 'Co znamena
