@@ -167,9 +167,10 @@ __host__ __device__ inline float plane_factor(int k) {
 // wavefront's load and its fp16 operands of four 16x16x32 MFMAs:
 //   lane L, word t holds row 16*rt + (L & 15), columns 128*kt + 32*t + 8*(L >> 4) + [0, 8);
 //   nibble p of the word is column 2p of the eight, nibble p + 4 column 2p + 1 (p < 4).
-// Codes of rows >= m or columns >= n are 0.  Scales and zero points (one byte)
-// are stored as [row tile][column tile][group of the tile][16 rows], 128 / G
-// groups a tile; entries that belong to no group are 0.
+// Codes of rows >= m or columns >= n are 0.  With SG = 128 / G groups a tile, a
+// tile's scales are stored as [4 quads of rows][SG groups][4 rows] (what a lane
+// needs for its four rows of a result lies together) and its zero points, a byte
+// each, as [16 rows][SG groups]; entries that belong to no group are 0.
 // Blob: header | codes | scales | zero points (if any), each 256-byte aligned.
 // ---------------------------------------------------------------------------
 constexpr uint32_t Q4_MAGIC = 0x3134514eu;  // "NQ41"

@@ -36,6 +36,15 @@ typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
 // halves that one mask takes out of the word, columns 2p and 2p + 1.
 __device__ inline int q4_nibble_col(int p) { return p < 4 ? 2 * p : 2 * (p - 4) + 1; }
 
+// Row of W and group of its row that an entry of the scales (quad = 4) or zero
+// points (quad = 1) belongs to.
+__device__ inline void q4_group_entry(long long id, int KT, int SG, int quad, int* row, int* g) {
+  const int within = (int)(id % (16 * SG));
+  const long long tile = id / (16 * SG);
+  *row = (int)(tile / KT) * 16 + within / (quad * SG) * quad + within % quad;
+  *g = (int)(tile % KT) * SG + within / quad % SG;
+}
+
 // One thread per 32-bit word of codes.
 __global__ void __launch_bounds__(256) q4_pack_codes_kernel(const uint8_t* __restrict__ q, int m, int n, int KT,
                                                             long long words, uint32_t* __restrict__ out,
@@ -60,14 +69,15 @@ __global__ void __launch_bounds__(256) q4_pack_codes_kernel(const uint8_t* __res
   }
 }
 
-// One thread per (row tile, column tile, group, row) entry of scales or zero points.
+// One thread per entry of the scales (quad = 4: four rows of a group together)
+// or the zero points (quad = 1: a row's groups together).
 template <typename T>
 __global__ void __launch_bounds__(256) q4_pack_groups_kernel(const T* __restrict__ in, int m, int ng, int KT, int SG,
-                                                             long long entries, T* __restrict__ out, int limit,
-                                                             int* __restrict__ bad_flag) {
+                                                             int quad, long long entries, T* __restrict__ out,
+                                                             int limit, int* __restrict__ bad_flag) {
   for (long long id = (long long)blockIdx.x * 256 + threadIdx.x; id < entries; id += (long long)gridDim.x * 256) {
-    const long long rest = id >> 4;
-    const int g = (int)(rest % (KT * SG)), row = (int)(rest / (KT * SG)) * 16 + (int)(id & 15);
+    int row, g;
+    q4_group_entry(id, KT, SG, quad, &row, &g);
     T v = 0;
     if (row < m && g < ng) v = in[(size_t)row * ng + g];
     if (limit && (int)v > limit) atomicOr(bad_flag, 1);
@@ -94,87 +104,169 @@ __global__ void __launch_bounds__(256) q4_unpack_kernel(const uint32_t* __restri
 __global__ void __launch_bounds__(256) q4_unpack_zeros_kernel(const uint8_t* __restrict__ in, int m, int ng, int KT,
                                                               int SG, long long entries, uint8_t* __restrict__ z) {
   for (long long id = (long long)blockIdx.x * 256 + threadIdx.x; id < entries; id += (long long)gridDim.x * 256) {
-    const long long rest = id >> 4;
-    const int g = (int)(rest % (KT * SG)), row = (int)(rest / (KT * SG)) * 16 + (int)(id & 15);
+    int row, g;
+    q4_group_entry(id, KT, SG, 1, &row, &g);
     if (row < m && g < ng) z[(size_t)row * ng + g] = in[id];
   }
 }
 
 // ------------------------------------------------------------------ shared pieces
+// A zero point ready for both places a code can have in a half: -(1024 + z) for
+// the four lowest bits of the mantissa, -(64 + z) for the four above them.
+struct Q4Zero {
+  h2 low, high;
+};
+__device__ __forceinline__ Q4Zero q4_zero(uint32_t z) {
+  const uint32_t zz = z | (z << 16);
+  return {__builtin_bit_cast(h2, zz | 0xE400E400u), __builtin_bit_cast(h2, (zz << 4) | 0xD400D400u)};
+}
+
+// The magic numbers of q4_expand, out of the compiler's sight: as constants they
+// would cost an instruction of their own at each use (an instruction takes one
+// constant; and-then-or would need two).
+struct Q4Magic {
+  uint32_t low = 0x64006400u, high = 0x54005400u;
+  __device__ __forceinline__ Q4Magic() { asm("" : "+v"(low), "+v"(high)); }
+};
+
 // The eight codes of a word less their zero point, as an MFMA operand: column
-// order 0..7.  zc holds -(1024 + z) twice.
-__device__ __forceinline__ h8 q4_expand(uint32_t w, h2 zc) {
+// order 0..7.  1024 + q is 0x6400 with q in the lowest bits, 64 + q is 0x5400
+// with q four bits up, so that of a word's four pairs only two need a shift:
+// nine instructions a word.
+__device__ __forceinline__ h8 q4_expand(uint32_t w, const Q4Zero& z, const Q4Magic& magic) {
   union {
     h2 p[4];
     h8 v;
   } u;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const uint32_t c = ((w >> (4 * i)) & 0x000F000Fu) | 0x64006400u;
-    u.p[i] = __builtin_bit_cast(h2, c) + zc;
-  }
+  const uint32_t v = w >> 8;
+  u.p[0] = __builtin_bit_cast(h2, (w & 0x000F000Fu) | magic.low) + z.low;
+  u.p[1] = __builtin_bit_cast(h2, (w & 0x00F000F0u) | magic.high) + z.high;
+  u.p[2] = __builtin_bit_cast(h2, (v & 0x000F000Fu) | magic.low) + z.low;
+  u.p[3] = __builtin_bit_cast(h2, (v & 0x00F000F0u) | magic.high) + z.high;
   return u.v;
 }
 
-__device__ __forceinline__ h2 q4_zero(uint32_t z) { return __builtin_bit_cast(h2, (z | (z << 16)) | 0xE400E400u); }
+// A lane's four rows of scales of every group of a tile, kept as they are stored
+// until they are used, and its row's zero points.
+template <typename ST, int SG>
+struct Q4Scales {
+  typedef ST v4 __attribute__((ext_vector_type(4)));
+  v4 v[SG];
+  __device__ __forceinline__ void load(const uint8_t* base, size_t tile, int lane) {
+    typedef ST row __attribute__((ext_vector_type(4 * SG)));
+    const row r = reinterpret_cast<const row*>(base)[tile * 4 + (lane >> 4)];
+#pragma unroll
+    for (int g = 0; g < SG; g++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[g][i] = r[4 * g + i];
+  }
+  __device__ __forceinline__ float get(int g, int i) const { return (float)v[g][i]; }
+};
+template <int SG, bool ZERO>
+struct Q4Zeros {
+  uint32_t z;
+  __device__ __forceinline__ void load(const uint8_t* base, size_t tile, int lane) {
+    if (!ZERO) return;
+    const size_t at = tile * 16 + (lane & 15);
+    z = SG == 1 ? base[at]
+        : SG == 2 ? reinterpret_cast<const uint16_t*>(base)[at] : reinterpret_cast<const uint32_t*>(base)[at];
+  }
+  __device__ __forceinline__ uint32_t get(int g) const { return !ZERO ? 8u : SG == 1 ? z : (z >> (8 * g)) & 255u; }
+};
 
-// Four neighbouring scales as floats.
-__device__ __forceinline__ v4f q4_scales(const _Float16* p) {
-  return __builtin_convertvector(*reinterpret_cast<const h4*>(p), v4f);
-}
-__device__ __forceinline__ v4f q4_scales(const float* p) { return *reinterpret_cast<const v4f*>(p); }
-
-// Columns k .. k+7 of a row of x (zero from column n on) as floats; vec: the
-// eight can be read in 16-byte pieces.
-__device__ __forceinline__ void q4_load8(const float* x, int k, int n, bool vec, float* v) {
-  if (vec && k + 8 <= n) {
-    const v4f a = *reinterpret_cast<const v4f*>(x + k), b = *reinterpret_cast<const v4f*>(x + k + 4);
+// Columns k .. k+7 of a row of x (zero from column n on), as they are stored
+// until get().  The 16-byte reads need not be aligned: a row of an odd width starts
+// anywhere.
+typedef float v4f_at4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
+template <typename XT>
+struct Q4X;
+template <>
+struct Q4X<float> {
+  v4f a, b;
+  __device__ __forceinline__ void load(const float* x, int k, int n) {
+    if (k + 8 <= n) {
+      a = *reinterpret_cast<const v4f_at4*>(x + k);
+      b = *reinterpret_cast<const v4f_at4*>(x + k + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        a[i] = k + i < n ? x[k + i] : 0.0f;
+        b[i] = k + 4 + i < n ? x[k + 4 + i] : 0.0f;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = k + i < n ? x[k + i] : 0.0f;
   }
-}
-__device__ __forceinline__ void q4_load8(const uint16_t* x, int k, int n, bool vec, float* v) {
-  if (vec && k + 8 <= n) {
-    const uint4 a = *reinterpret_cast<const uint4*>(x + k);
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+  // bits of the largest magnitude; FINITE: of the largest below infinity
+  template <bool FINITE>
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t u = __float_as_uint(i < 4 ? a[i & 3] : b[i & 3]) & 0x7fffffffu;
+      mx = max(mx, FINITE && u >= 0x7f800000u ? 0u : u);
+    }
+    return mx;
+  }
+};
+template <>
+struct Q4X<uint16_t> {
+  u32x4 a;
+  __device__ __forceinline__ void load(const uint16_t* x, int k, int n) {
+    if (k + 8 <= n) {
+      a = *reinterpret_cast<const u32x4_at2*>(x + k);
+    } else {
+      uint32_t u[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) u[i] = k + i < n ? x[k + i] : 0u;
+      a = u32x4{u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16};
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = k + i < n ? to_f32<uint16_t>(x[k + i]) : 0.0f;
   }
-}
-
-// Largest finite magnitude of eight values (0 if there is none).
-__device__ __forceinline__ float q4_max8(const float* v) {
-  float mx = 0.0f;
+  template <bool FINITE>
+  __device__ __forceinline__ uint32_t top() const {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 mx = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float a = fabsf(v[i]);
-    mx = fmaxf(mx, a < INFINITY ? a : 0.0f);
+    for (int i = 0; i < 4; i++) {
+      u16x2 v = __builtin_bit_cast(u16x2, a[i] & 0x7fff7fffu);
+      if (FINITE) {
+        v[0] = v[0] >= 0x7f80 ? 0 : v[0];
+        v[1] = v[1] >= 0x7f80 ? 0 : v[1];
+      }
+      mx = __builtin_elementwise_max(mx, v);
+    }
+    return (uint32_t)max(mx[0], mx[1]) << 16;
   }
-  return mx;
+};
+
+// Power of two that puts a block whose largest magnitude has these bits (of an
+// fp32 number, below infinity) into fp16: the largest times 2^e lies in
+// [2^14, 2^15).  e <= 120 keeps 2^-e a normal number.
+__device__ __forceinline__ int q4_block_exp(uint32_t mx) {
+  const int e = 14 + 127 - (int)(mx >> 23);
+  return mx == 0 ? 0 : e < 120 ? e : 120;
 }
 
-// Power of two that puts a block whose largest magnitude is mx into fp16: mx 2^e
-// in [2^14, 2^15).  e <= 120 keeps 2^-e a normal number.
-__device__ __forceinline__ int q4_block_exp(float mx) {
-  if (!(mx > 0.0f)) return 0;
-  const int e = 14 - floor_log2(mx);
-  return e < 120 ? e : 120;
-}
+// 2^e as a float, -126 <= e <= 127.
+__device__ __forceinline__ float q4_exp2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// v 2^e as fp16 (f = 2^e), with P = 2 its remainder too.
 template <int P>
-__device__ __forceinline__ void q4_to_f16(const float* v, int e, h8* hi, h8* lo) {
+__device__ __forceinline__ void q4_to_f16(const float* v, float f, h8* hi, h8* lo) {
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float s = __builtin_ldexpf(v[i], e);
+    const float s = v[i] * f;
     const _Float16 h = (_Float16)s;
     (*hi)[i] = h;
     // an infinity or NaN has no remainder
@@ -183,9 +275,8 @@ __device__ __forceinline__ void q4_to_f16(const float* v, int e, h8* hi, h8* lo)
 }
 
 // Maximum over the 16 lanes of a row of the wavefront.
-__device__ __forceinline__ float row16_max(float v) {
-#define NQ_ROR_MAX(n)                                                                                           \
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + (n), 0xf, 0xf, false)))
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+#define NQ_ROR_MAX(n) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + (n), 0xf, 0xf, false))
   NQ_ROR_MAX(8);
   NQ_ROR_MAX(4);
   NQ_ROR_MAX(2);
@@ -199,181 +290,303 @@ __device__ __forceinline__ void q4_store(void* y, int ydt, size_t i, float v) {
   else reinterpret_cast<uint16_t*>(y)[i] = f32_to_bf16(v);
 }
 
-// Orders a wavefront's own shared-memory accesses before and after it.
-__device__ __forceinline__ void wave_lds_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // ------------------------------------------------------------------ decode: B <= 16
+struct Q4DecLayer {
+  const uint8_t *codes, *scales, *zeros;
+  void* out;    // y, or with S > 1 the first split's partial sums
+  int m, rt_end;  // rows; row tiles up to this layer's end, counted through
+};
 struct Q4DecArgs {
-  const uint8_t* blob[GROUP_MAX];
-  void* y[GROUP_MAX];
-  int m[GROUP_MAX], wg_end[GROUP_MAX];
-  int L, n, KT, B;
-  int tpw;     // column tiles per wave
-  int region;  // bytes of shared memory per wave
-  int xvec, ydt;
+  Q4DecLayer layer[GROUP_MAX];
   const void* x;
+  int n, KT, B, rows;     // rows: row tiles of all layers
+  int range, tpw, steps;  // column tiles of a split, of a wave; units of a wave's row tile
+  int shared;             // the waves share each row tile; else each has its own
+  int groups;             // workgroups of one split
+  int keep;               // row tiles whose shared sums are kept before they are added
+  int odt;                // dtype of out
+  size_t part_split;      // values between the splits' partial sums
 };
 
-// One workgroup computes R row tiles (16 R rows) of one layer for all B <= 16
-// rows of x; its waves take contiguous runs of tpw column tiles each and their
-// sums meet in shared memory.  A wave goes through its run T column tiles at a
-// time: it asks for the codes, scales and zero points of R x T tiles, turns the
-// same columns of x into fp16 in its own part of shared memory while they
-// come, and multiplies.  Lane layout of the 16x16x32 MFMA: the first operand
-// has row lane & 15 and columns 8 (lane >> 4) .. + 7, the second row b = lane & 15
-// of x and the same columns; the result has row 4 (lane >> 4) + v of the tile
-// for b = lane & 15.  Lanes with b >= B repeat row B - 1 and are not stored.
-template <typename XT, typename ST, int SG, bool ZERO, int T, int R>
+// The codes, scales and zero points of one tile, as one lane holds them.
+template <typename ST, int SG, bool ZERO>
+struct Q4Tile {
+  uint4 w;
+  Q4Scales<ST, SG> sc;
+  Q4Zeros<SG, ZERO> z;
+};
+
+// A workgroup of W waves holds the columns of its split of x as fp16 in shared
+// memory and goes through row tiles.  Either all waves share a row tile, each a
+// run of tpw column tiles, and their sums meet in shared memory, or (shared = 0)
+// each wave has a row tile to itself.  A wave's tiles, row tile after row tile,
+// are one sequence of units of U tiles; a ring of D units is in flight, and a
+// place of the ring is asked for anew as soon as its unit has been multiplied, so
+// that the reads do not pause for the sums at the end of a row tile.  Lane layout
+// of the 16x16x32 MFMA: the first operand has row lane & 15 and columns
+// 8 (lane >> 4) .. + 7, the second row b = lane & 15 of x and the same columns; the
+// result has row 4 (lane >> 4) + v of the tile for b = lane & 15.  Lanes with
+// b >= B repeat row B - 1 and are not stored.
+template <typename XT, typename ST, int SG, bool ZERO, int U, int D>
 __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
   constexpr int P = sizeof(XT) == 4 ? 2 : 1;
+  constexpr int XN = 8 / P;  // pieces of x that a thread reads at a time
+  constexpr int PRE = (U + 1) / 2;
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, W = blockDim.x >> 6, B = a.B, KT = a.KT;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint8_t* mine = smem + wave * a.region;
-  _Float16* img = reinterpret_cast<_Float16*>(mine);                        // [P][T][B][128]
-  float* xfac = reinterpret_cast<float*>(mine + (size_t)P * T * B * 256);  // [T][B]
+  const int split = blockIdx.x / a.groups, group = blockIdx.x % a.groups;
+  const int k_lo = split * a.range, k_hi = min(KT, k_lo + a.range), KR = a.range;
+  _Float16* img = reinterpret_cast<_Float16*>(smem);                        // [P][KR][B][128]
+  float* xfac = reinterpret_cast<float*>(smem + (size_t)P * KR * B * 256);  // [KR][B]
+  float* red = xfac + KR * B;                                               // [keep][W][B][16]
 
-  int l = 0, wg = blockIdx.x;
-  while (l + 1 < a.L && (int)blockIdx.x >= a.wg_end[l]) l++;
-  if (l) wg -= a.wg_end[l - 1];
-  const int m = a.m[l], RT = ceil_div(m, 16), rt0 = wg * R;
-  const Q4Layout lay = q4_layout(m, a.n, 128 / SG, sizeof(ST), ZERO);
-  const uint8_t* blob = a.blob[l];
-  const XT* x = reinterpret_cast<const XT*>(a.x);
+  const bool shared = a.shared;
+  const int wr = shared ? 0 : wave, WR = shared ? 1 : W;
+  const int kbeg = k_lo + (shared ? wave * a.tpw : 0), kend = min(k_hi, kbeg + a.tpw);
+  const int rows = a.rows, stride = a.groups * WR, first = group * WR;
+  // row tiles that the workgroup goes through (wave 0 has most) and units of a
+  // wave's sequence, the same for every wave: the barriers are met by all
+  const int turns = (rows - first + stride - 1) / stride;
+  int to_ask = turns * a.steps;
 
-  const uint4* codes[R];
-  const ST* scales[R];
-  const uint8_t* zeros[R];
-#pragma unroll
-  for (int r = 0; r < R; r++) {
-    const size_t rt = min(rt0 + r, RT - 1);
-    codes[r] = reinterpret_cast<const uint4*>(blob + lay.off_codes) + rt * KT * 64 + lane;
-    scales[r] = reinterpret_cast<const ST*>(blob + lay.off_scales) + rt * KT * SG * 16 + 4 * (lane >> 4);
-    zeros[r] = blob + lay.off_zeros + rt * KT * SG * 16 + (lane & 15);
-  }
-  v4f acc[R];
-#pragma unroll
-  for (int r = 0; r < R; r++) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
-
-  const int kbeg = wave * a.tpw, kend = min(KT, kbeg + a.tpw);
-  const int bc = min(lane & 15, B - 1);
-  for (int k0 = kbeg; k0 < kend; k0 += T) {
-    uint4 w[R][T];
-    v4f sc[R][T][SG];
-    uint32_t z[R][T][SG];
-#pragma unroll
-    for (int t = 0; t < T; t++) {
-      const int kt = min(k0 + t, kend - 1);
-#pragma unroll
-      for (int r = 0; r < R; r++) {
-        w[r][t] = codes[r][(size_t)kt * 64];
-#pragma unroll
-        for (int g = 0; g < SG; g++) {
-          sc[r][t][g] = q4_scales(scales[r] + (kt * SG + g) * 16);
-          if (ZERO) z[r][t][g] = zeros[r][(kt * SG + g) * 16];
-        }
-      }
+  // ---- the sequence of units to be asked for.  A layer's pointers are read anew
+  // only where one layer ends and the next begins.
+  Q4Tile<ST, SG, ZERO> ring[D][U];
+  const uint8_t *codes = a.layer[0].codes, *scales = a.layer[0].scales, *zeros = a.layer[0].zeros;
+  int ask_l = 0, ask_lo = 0, ask_hi = a.layer[0].rt_end, ask_rt = first + wr, ask_step = 0;
+  size_t ask_tile;
+  auto seek = [&]() {
+    const int rt = min(ask_rt, rows - 1);
+    while (rt >= ask_hi) {
+      ask_l++;
+      ask_lo = ask_hi;
+      ask_hi = a.layer[ask_l].rt_end;
+      codes = a.layer[ask_l].codes;
+      scales = a.layer[ask_l].scales;
+      zeros = a.layer[ask_l].zeros;
     }
-    // x: sixteen lanes take the 128 columns of one (row, tile), eight each; the
-    // 16-byte pieces of row b are stored exchanged by b so that the sixteen rows
-    // of an operand read lie in different banks
-    for (int u = lane >> 4; u < T * B; u += 4) {
-      const int t = u % T, b = u / T, j = lane & 15, kt = k0 + t;
-      if (kt >= kend) continue;
-      float v[8];
-      q4_load8(x + (size_t)b * a.n, kt * 128 + 8 * j, a.n, a.xvec, v);
-      const int e = q4_block_exp(row16_max(q4_max8(v)));
-      h8 hi, lo;
-      q4_to_f16<P>(v, e, &hi, &lo);
-      const int at = ((t * B + b) * 16 + (j ^ (b & 15))) * 8;
-      *reinterpret_cast<h8*>(img + at) = hi;
-      if (P == 2) *reinterpret_cast<h8*>(img + T * B * 128 + at) = lo;
-      if (j == 0) xfac[t * B + b] = __builtin_ldexpf(1.0f, -e);
+    ask_tile = (size_t)(rt - ask_lo) * KT;
+  };
+  auto load = [&](Q4Tile<ST, SG, ZERO>& q, int t) {
+    // past the run its last tile is asked for again
+    const size_t tile = ask_tile + max(min(kbeg + ask_step * U + t, kend - 1), 0);
+    q.w = reinterpret_cast<const uint4*>(codes + tile * 1024)[lane];
+    q.sc.load(scales, tile, lane);
+    q.z.load(zeros, tile, lane);
+  };
+  auto asked = [&]() {  // a whole unit
+    to_ask--;
+    if (++ask_step == a.steps) {
+      ask_step = 0;
+      ask_rt += stride;
+      seek();
     }
-    wave_lds_order();
+  };
+  // ---- x: sixteen lanes take the 128 columns of one (tile, row), eight each; the
+  // 16-byte pieces of row b are stored exchanged by b so that the sixteen rows
+  // of an operand read lie in different banks.  All of x is asked for before any
+  // code: behind the codes of the other waves it would come microseconds later.
+  const int units = turns * a.steps;
+  {
+    const XT* x = reinterpret_cast<const XT*>(a.x);
+    const int j = lane & 15, pieces = (k_hi - k_lo) * B, by = blockDim.x >> 4;
+    Q4X<XT> raw[XN];
+    auto fetch = [&](int u0, int count) {
 #pragma unroll
-    for (int t = 0; t < T; t++) {
-      if (k0 + t >= kend) break;
-      h8 bh[4], bl[4];
-#pragma unroll
-      for (int s = 0; s < 4; s++) {
-        const int at = ((t * B + bc) * 16 + ((4 * s + (lane >> 4)) ^ (bc & 15))) * 8;
-        bh[s] = *reinterpret_cast<const h8*>(img + at);
-        if (P == 2) bl[s] = *reinterpret_cast<const h8*>(img + T * B * 128 + at);
+      for (int i = 0; i < XN; i++) {
+        if (i >= count) break;
+        const int u = min(u0 + i * by, pieces - 1);
+        raw[i].load(x + (size_t)(u % B) * a.n, (k_lo + u / B) * 128 + 8 * j, a.n);
       }
-      const float f = xfac[t * B + bc];
+    };
+    auto turn_over = [&](int u0, int count) {
 #pragma unroll
-      for (int r = 0; r < R; r++) {
-        const uint32_t ww[4] = {w[r][t].x, w[r][t].y, w[r][t].z, w[r][t].w};
-#pragma unroll
-        for (int g = 0; g < SG; g++) {
-          const h2 zc = q4_zero(ZERO ? z[r][t][g] : 8u);
-          v4f d{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = g * 4 / SG; s < (g + 1) * 4 / SG; s++) {
-            const h8 av = q4_expand(ww[s], zc);
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bh[s], d, 0, 0, 0);
-            if (P == 2) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bl[s], d, 0, 0, 0);
-          }
-          const v4f sf = sc[r][t][g] * f;
-#pragma unroll
-          for (int v = 0; v < 4; v++) acc[r][v] = fmaf(sf[v], d[v], acc[r][v]);
-        }
+      for (int i = 0; i < XN; i++) {
+        if (i >= count) break;
+        const int u = u0 + i * by;
+        uint32_t mx = row16_max(raw[i].template top<false>());
+        if (mx >= 0x7f800000u) mx = row16_max(raw[i].template top<true>());
+        const int e = q4_block_exp(mx);
+        float v[8];
+        raw[i].get(v);
+        h8 hi, lo;
+        q4_to_f16<P>(v, q4_exp2(e), &hi, &lo);
+        if (u >= pieces) continue;
+        const int at = (u * 16 + (j ^ (u % B & 15))) * 8;
+        *reinterpret_cast<h8*>(img + at) = hi;
+        if (P == 2) *reinterpret_cast<h8*>(img + (size_t)KR * B * 128 + at) = lo;
+        if (j == 0) xfac[u] = q4_exp2(-e);
       }
+    };
+    int u0 = threadIdx.x >> 4, left = ceil_div(pieces, by);
+    for (; left > XN; left -= XN, u0 += XN * by) {
+      fetch(u0, XN);
+      turn_over(u0, XN);
     }
-    wave_lds_order();
-  }
-
-  // the waves' sums: [row][b] in each wave's own region, added in wave order
-  float* red = reinterpret_cast<float*>(mine);
-  if ((lane & 15) < B) {
+    fetch(u0, left);
+    __builtin_amdgcn_s_barrier();
+    seek();
 #pragma unroll
-    for (int r = 0; r < R; r++)
-#pragma unroll
-      for (int v = 0; v < 4; v++) red[(r * 16 + 4 * (lane >> 4) + v) * B + (lane & 15)] = acc[r][v];
+    for (int t = 0; t < PRE; t++) load(ring[0][t], t);
+    turn_over(u0, left);
   }
+#pragma unroll
+  for (int t = PRE; t < U; t++) load(ring[0][t], t);
+  asked();
   __syncthreads();
-  for (int id = threadIdx.x; id < 16 * R * B; id += blockDim.x) {
-    const int row = id % (16 * R), b = id / (16 * R), i = rt0 * 16 + row;
-    if (i >= m) continue;
-    float s = 0.0f;
-    for (int w = 0; w < W; w++) s += *reinterpret_cast<const float*>(smem + w * a.region + (row * B + b) * 4);
-    q4_store(a.y[l], a.ydt, (size_t)b * m + i, s);
+#pragma unroll
+  for (int i = 1; i < D; i++) {
+#pragma unroll
+    for (int t = 0; t < U; t++) load(ring[i][t], t);
+    asked();
   }
+
+  // ---- the sequence of units to be multiplied
+  const Q4Magic magic;
+  const int bc = min(lane & 15, B - 1);
+  int step = 0, rt = first + wr, kept = 0;
+  v4f acc{0.f, 0.f, 0.f, 0.f};
+  int out_l = 0, out_lo = 0, out_hi = a.layer[0].rt_end, out_m = a.layer[0].m;
+  void* out = a.layer[0].out;
+  const size_t out_split = split * a.part_split;
+  auto put = [&](int rt, int row, int b, float v) {
+    while (rt >= out_hi) {
+      out_l++;
+      out_lo = out_hi;
+      out_hi = a.layer[out_l].rt_end;
+      out_m = a.layer[out_l].m;
+      out = a.layer[out_l].out;
+    }
+    const int i = (rt - out_lo) * 16 + row;
+    if (i < out_m) q4_store(out, a.odt, out_split + (size_t)b * out_m + i, v);
+  };
+  // The end of a row tile.  A wave that has it to itself stores its sums.  Shared
+  // sums are kept in shared memory, a.keep row tiles of them, and added when it is
+  // full or all row tiles are done, so that the waves seldom wait for each other:
+  // four lanes add a quarter of the waves' sums each, then the four.
+  auto finish = [&]() {
+    if (!shared) {
+      if (rt < rows)
+#pragma unroll
+        for (int v = 0; v < 4; v++)
+          if ((lane & 15) < B) put(rt, 4 * (lane >> 4) + v, lane & 15, acc[v]);
+    } else {
+      if ((lane & 15) < B)
+        *reinterpret_cast<v4f*>(red + ((kept * W + wave) * B + (lane & 15)) * 16 + 4 * (lane >> 4)) = acc;
+      kept++;
+      if (kept == a.keep || rt + stride >= rows) {
+        __syncthreads();
+        const int rt0 = rt - (kept - 1) * stride;
+        for (int id = wave; id < kept * B; id += W) {
+          const int i = id / B, b = id % B;
+          const float* r = red + (i * W * B + b) * 16 + (lane & 15);
+          float s = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            const int w = 4 * q + (lane >> 4);
+            if (w < W) s += r[w * B * 16];
+          }
+          s += __shfl_xor(s, 16);
+          s += __shfl_xor(s, 32);
+          if (lane < 16) put(rt0 + i * stride, lane, b, s);
+        }
+        kept = 0;
+        __syncthreads();
+      }
+    }
+    acc = v4f{0.f, 0.f, 0.f, 0.f};
+    rt += stride;
+  };
+  auto multiply = [&](const Q4Tile<ST, SG, ZERO>& q, int t) {
+    const int kt = kbeg + step * U + t;
+    if (kt >= kend) return;
+    const int u = (kt - k_lo) * B + bc;
+    h8 bh[4], bl[4];
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+      const int at = (u * 16 + ((4 * s + (lane >> 4)) ^ (bc & 15))) * 8;
+      bh[s] = *reinterpret_cast<const h8*>(img + at);
+      if (P == 2) bl[s] = *reinterpret_cast<const h8*>(img + (size_t)KR * B * 128 + at);
+    }
+    const float f = xfac[u];
+    const uint32_t ww[4] = {q.w.x, q.w.y, q.w.z, q.w.w};
+#pragma unroll
+    for (int g = 0; g < SG; g++) {
+      const Q4Zero zc = q4_zero(q.z.get(g));
+      v4f d{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = g * 4 / SG; s < (g + 1) * 4 / SG; s++) {
+        const h8 av = q4_expand(ww[s], zc, magic);
+        d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bh[s], d, 0, 0, 0);
+        if (P == 2) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bl[s], d, 0, 0, 0);
+      }
+      // f is a power of two: d f is exact
+#pragma unroll
+      for (int v = 0; v < 4; v++) acc[v] = fmaf(q.sc.get(g, v), d[v] * f, acc[v]);
+    }
+  };
+  auto multiplied = [&]() {  // a whole unit
+    if (++step == a.steps) {
+      step = 0;
+      finish();
+    }
+  };
+
+  // rounds of the ring, then the units that are left in it.  What a last round
+  // asks for past the end is the last row tile, which the L2 holds by then.
+  int left = units;
+  for (; to_ask > 0; left -= D)
+#pragma unroll
+    for (int i = 0; i < D; i++) {
+#pragma unroll
+      for (int t = 0; t < U; t++) {
+        multiply(ring[i][t], t);
+        load(ring[i][t], t);
+      }
+      asked();
+      multiplied();
+    }
+#pragma unroll
+  for (int i = 0; i < D; i++)
+    if (i < left) {
+#pragma unroll
+      for (int t = 0; t < U; t++) multiply(ring[i][t], t);
+      multiplied();
+    }
 }
 
 // ------------------------------------------------------------------ prompts: any B
 // x as fp16 rows of Kpad columns (zero from column n on) with one power of two a
 // row; for fp32 x the remainders follow as a second image.
 template <typename XT>
-__global__ void __launch_bounds__(256) q4_rows_kernel(const XT* __restrict__ x, int n, int Kpad, int xvec,
+__global__ void __launch_bounds__(256) q4_rows_kernel(const XT* __restrict__ x, int n, int Kpad,
                                                       _Float16* __restrict__ hi, _Float16* __restrict__ lo,
                                                       float* __restrict__ fac) {
   constexpr int P = sizeof(XT) == 4 ? 2 : 1;
-  __shared__ float red[4];
+  __shared__ uint32_t red[4];
   const size_t row = blockIdx.x;
   const XT* src = x + row * n;
-  float mx = 0.0f, v[8];
+  uint32_t mx = 0;
+  Q4X<XT> raw;
   for (int k = 8 * threadIdx.x; k < n; k += 2048) {
-    q4_load8(src, k, n, xvec, v);
-    mx = fmaxf(mx, q4_max8(v));
+    raw.load(src, k, n);
+    mx = max(mx, raw.template top<true>());
   }
-  for (int o = 32; o; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
+  for (int o = 32; o; o >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
   __syncthreads();
-  mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const int e = q4_block_exp(mx);
+  const int e = q4_block_exp(max(max(red[0], red[1]), max(red[2], red[3])));
   for (int k = 8 * threadIdx.x; k < Kpad; k += 2048) {
+    float v[8];
     h8 h, r;
-    q4_load8(src, k, n, xvec, v);
-    q4_to_f16<P>(v, e, &h, &r);
+    raw.load(src, k, n);
+    raw.get(v);
+    q4_to_f16<P>(v, q4_exp2(e), &h, &r);
     *reinterpret_cast<h8*>(hi + row * Kpad + k) = h;
     if (P == 2) *reinterpret_cast<h8*>(lo + row * Kpad + k) = r;
   }
-  if (threadIdx.x == 0) fac[row] = __builtin_ldexpf(1.0f, -e);
+  if (threadIdx.x == 0) fac[row] = q4_exp2(-e);
 }
 
 struct Q4GemmArgs {
@@ -409,16 +622,10 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
   const Q4Layout lay = q4_layout(a.m, a.n, 128 / SG, sizeof(ST), ZERO);
   const int wm = (wave >> 1) * 64, wb = (wave & 1) * 64;
 
-  const uint4* codes[4];
-  const ST* scales[4];
-  const uint8_t* zeros[4];
+  const uint8_t *codes = a.blob + lay.off_codes, *scales = a.blob + lay.off_scales, *zeros = a.blob + lay.off_zeros;
+  size_t row_tile[4];  // first tile of the wave's row tiles
 #pragma unroll
-  for (int r = 0; r < 4; r++) {
-    const size_t rt = min((i0 + wm) / 16 + r, RT - 1);
-    codes[r] = reinterpret_cast<const uint4*>(a.blob + lay.off_codes) + rt * KT * 64 + lane;
-    scales[r] = reinterpret_cast<const ST*>(a.blob + lay.off_scales) + rt * KT * SG * 16 + 4 * (lane >> 4);
-    zeros[r] = a.blob + lay.off_zeros + rt * KT * SG * 16 + (lane & 15);
-  }
+  for (int r = 0; r < 4; r++) row_tile[r] = (size_t)min((i0 + wm) / 16 + r, RT - 1) * KT;
   // x tile: 128 rows x 16 pieces of 16 bytes; piece c of row b lies at place
   // c ^ (b & 15) of the row (see the decode kernel), so the place is fixed by the
   // thread and the column it reads from by the exchange
@@ -440,13 +647,18 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
 #pragma unroll
     for (int c = 0; c < 4; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  const Q4Magic magic;
   if (kbeg < kend) stage(kbeg, 0);
   __syncthreads();
   for (int kt = kbeg; kt < kend; kt++) {
     const int buf = (kt - kbeg) & 1;
-    uint4 w[4];
+    Q4Tile<ST, SG, ZERO> w[4];
 #pragma unroll
-    for (int r = 0; r < 4; r++) w[r] = codes[r][(size_t)kt * 64];
+    for (int r = 0; r < 4; r++) {
+      w[r].w = reinterpret_cast<const uint4*>(codes + (row_tile[r] + kt) * 1024)[lane];
+      w[r].sc.load(scales, row_tile[r] + kt, lane);
+      w[r].z.load(zeros, row_tile[r] + kt, lane);
+    }
     if (kt + 1 < kend) stage(kt + 1, buf ^ 1);
 #pragma unroll
     for (int g = 0; g < SG; g++) {
@@ -455,9 +667,9 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
       for (int r = 0; r < 4; r++)
 #pragma unroll
         for (int c = 0; c < 4; c++) d[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
-      h2 zc[4];
+      Q4Zero zc[4];
 #pragma unroll
-      for (int r = 0; r < 4; r++) zc[r] = q4_zero(ZERO ? zeros[r][(kt * SG + g) * 16] : 8u);
+      for (int r = 0; r < 4; r++) zc[r] = q4_zero(w[r].z.get(g));
 #pragma unroll
       for (int s = g * 4 / SG; s < (g + 1) * 4 / SG; s++) {
         h8 bv[P][4];
@@ -471,7 +683,7 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
           }
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-          const h8 av = q4_expand(s == 0 ? w[r].x : s == 1 ? w[r].y : s == 2 ? w[r].z : w[r].w, zc[r]);
+          const h8 av = q4_expand(s == 0 ? w[r].w.x : s == 1 ? w[r].w.y : s == 2 ? w[r].w.z : w[r].w.w, zc[r], magic);
 #pragma unroll
           for (int p = 0; p < P; p++)
 #pragma unroll
@@ -480,11 +692,10 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
       }
 #pragma unroll
       for (int r = 0; r < 4; r++) {
-        const v4f sc = q4_scales(scales[r] + (kt * SG + g) * 16);
 #pragma unroll
         for (int c = 0; c < 4; c++)
 #pragma unroll
-          for (int v = 0; v < 4; v++) acc[r][c][v] = fmaf(sc[v], d[r][c][v], acc[r][c][v]);
+          for (int v = 0; v < 4; v++) acc[r][c][v] = fmaf(w[r].sc.get(g, v), d[r][c][v], acc[r][c][v]);
       }
     }
     __syncthreads();
@@ -507,25 +718,17 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
   }
 }
 
-// y = the S partial sums added in order.
-__global__ void __launch_bounds__(256) q4_join_kernel(const float* __restrict__ part, int S, size_t count, void* y,
-                                                      int ydt) {
+// y = the S partial sums, `stride` values apart, added in order.
+__global__ void __launch_bounds__(256) q4_join_kernel(const float* __restrict__ part, int S, size_t stride,
+                                                      size_t count, void* y, int ydt) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= count) return;
   float s = part[i];
-  for (int k = 1; k < S; k++) s += part[k * count + i];
+  for (int k = 1; k < S; k++) s += part[k * stride + i];
   q4_store(y, ydt, i, s);
 }
 
 // ------------------------------------------------------------------ host
-template <typename XT, typename ST, int SG, bool ZERO, int T>
-hipError_t launch_dec(const Q4DecArgs& a, int R, dim3 grid, int W, hipStream_t s) {
-  const size_t lds = (size_t)W * a.region;
-  if (R == 2) hipLaunchKernelGGL((q4_dec_kernel<XT, ST, SG, ZERO, T, 2>), grid, dim3(64 * W), lds, s, a);
-  else hipLaunchKernelGGL((q4_dec_kernel<XT, ST, SG, ZERO, T, 1>), grid, dim3(64 * W), lds, s, a);
-  return hipGetLastError();
-}
-
 // Calls f with the compile-time scale type, groups per tile and zero points.
 template <typename F>
 auto q4_dispatch(int scale_dtype, int group, bool zeros, F f) {
@@ -540,6 +743,8 @@ auto q4_dispatch(int scale_dtype, int group, bool zeros, F f) {
   return scale_dtype == 1 ? by_group(_Float16{}) : by_group(float{});
 }
 
+constexpr size_t MAX_LDS = 160 * 1024;
+
 // Workgroups of a pack kernel: its threads stride over the words, so that the
 // launch stays far below 2^32 threads for every weight.
 dim3 q4_pack_grid(long long items) {
@@ -547,42 +752,105 @@ dim3 q4_pack_grid(long long items) {
   return dim3((unsigned)(g < (1 << 20) ? g : (1 << 20)));
 }
 
+// Splits and shared memory of the decode kernel for B <= 16 rows of x.
+struct Q4DecPlan {
+  int W, S, range, tpw, groups, keep;
+  bool shared;
+  size_t lds, part;  // bytes: shared memory of a workgroup, partial sums
+};
+
+Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
+  Q4DecPlan p{};
+  const int KT = ceil_div(n, 128);
+  int RT = 0;
+  size_t out = 0;
+  for (int l = 0; l < L; l++) {
+    RT += ceil_div(m[l], 16);
+    out += (size_t)B * m[l];
+  }
+  const size_t per_tile = (size_t)B * (256 * P + 4);  // of the image of x
+  p.shared = per_tile * KT <= 112 * 1024;
+  if (p.shared) {
+    // the whole row of x fits: the waves of a workgroup share each row tile, four
+    // column tiles a wave where there are as many
+    const int w = ceil_div(KT, 4);
+    p.W = w < 16 ? w : 16;
+    p.S = 1;
+    // 16 waves a CU
+    const int fill = 256 * (16 / p.W);
+    p.groups = RT < fill ? RT : fill;
+  } else {
+    // a wave keeps its row tile; the columns are split so that the image fits
+    // and the workgroups fill the CUs
+    p.W = RT >= 256 ? 16 : 4;
+    const int row_groups = ceil_div(RT, p.W);
+    p.S = (int)((per_tile * KT + 144 * 1024 - 1) / (144 * 1024));
+    while (row_groups * p.S < 256 && ceil_div(KT, p.S) >= 8) p.S++;
+    p.groups = row_groups;
+  }
+  p.range = ceil_div(KT, p.S);
+  p.S = ceil_div(KT, p.range);
+  p.tpw = p.shared ? ceil_div(p.range, p.W) : p.range;
+  p.lds = per_tile * p.range;
+  if (p.shared) {
+    const int turns = ceil_div(RT, p.groups), each = p.W * 16 * B * 4;
+    const int fit = (int)((MAX_LDS - p.lds) / each);
+    p.keep = turns < fit ? turns : fit;
+    p.lds += (size_t)p.keep * each;
+  }
+  p.part = p.S > 1 ? p.S * out * 4 : 0;
+  return p;
+}
+
 template <typename XT>
 hipError_t dec_chunk(const Q4Args& a, int b0, int B) {
   constexpr int P = sizeof(XT) == 4 ? 2 : 1;
+  const Q4DecPlan p = q4_dec_plan(a.m, a.L, a.n, B, P);
   Q4DecArgs k{};
-  k.L = a.L;
   k.n = a.n;
   k.KT = ceil_div(a.n, 128);
   k.B = B;
-  k.ydt = a.y_dtype;
+  k.range = p.range;
+  k.tpw = p.tpw;
+  k.shared = p.shared;
+  k.groups = p.groups;
+  k.keep = p.keep;
+  k.odt = p.S > 1 ? 0 : a.y_dtype;
   const XT* x = static_cast<const XT*>(a.x) + (size_t)b0 * a.n;
   k.x = x;
-  k.xvec = a.n % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
-  int RT = 0;
-  for (int l = 0; l < a.L; l++) RT += ceil_div(a.m[l], 16);
-  const int R = RT >= 512 ? 2 : 1;
-  const int W = k.KT >= 16 ? 16 : k.KT;
-  const int T = B * P <= 8 ? 4 : B * P <= 16 ? 2 : 1;
-  k.tpw = ceil_div(k.KT, W);
-  const int image = T * B * (256 * P + 4), sums = 16 * R * B * 4;
-  k.region = (int)align_up(image > sums ? image : sums, 16);
-  int end = 0;
+  float* part = reinterpret_cast<float*>(a.ws);
+  void* y[GROUP_MAX];
   for (int l = 0; l < a.L; l++) {
-    k.blob[l] = a.blob[l];
-    k.y[l] = static_cast<uint8_t*>(a.y[l]) + (size_t)b0 * a.m[l] * (a.y_dtype == 0 ? 4 : 2);
-    k.m[l] = a.m[l];
-    end += ceil_div(ceil_div(a.m[l], 16), R);
-    k.wg_end[l] = end;
+    const Q4Layout lay = q4_layout(a.m[l], a.n, a.group, a.scale_dtype == 1 ? 2 : 4, a.zeros);
+    y[l] = static_cast<uint8_t*>(a.y[l]) + (size_t)b0 * a.m[l] * (a.y_dtype == 0 ? 4 : 2);
+    Q4DecLayer& c = k.layer[l];
+    c.codes = a.blob[l] + lay.off_codes;
+    c.scales = a.blob[l] + lay.off_scales;
+    c.zeros = a.blob[l] + lay.off_zeros;
+    c.out = p.S > 1 ? static_cast<void*>(part + k.part_split) : y[l];
+    c.m = a.m[l];
+    k.rows += ceil_div(a.m[l], 16);
+    c.rt_end = k.rows;
+    k.part_split += (size_t)B * a.m[l];
   }
-  return q4_dispatch(a.scale_dtype, a.group, a.zeros, [&](auto st, auto sg, auto zero) {
+  q4_dispatch(a.scale_dtype, a.group, a.zeros, [&](auto st, auto sg, auto zero) {
     using ST = decltype(st);
-    constexpr int SG = decltype(sg)::value;
-    constexpr bool Z = decltype(zero)::value;
-    return T == 4   ? launch_dec<XT, ST, SG, Z, 4>(k, R, dim3(end), W, a.stream)
-           : T == 2 ? launch_dec<XT, ST, SG, Z, 2>(k, R, dim3(end), W, a.stream)
-                    : launch_dec<XT, ST, SG, Z, 1>(k, R, dim3(end), W, a.stream);
+    constexpr int SG = decltype(sg)::value, bytes = SG * sizeof(ST);
+    // tiles in flight (U D): as many as the registers of 16 waves a CU hold beside
+    // the operands
+    constexpr int U = bytes == 2 ? 4 : bytes <= 8 ? 2 : 1, D = bytes == 4 || bytes == 16 ? 3 : 2;
+    k.steps = ceil_div(p.tpw, U);
+    auto kernel = q4_dec_kernel<XT, ST, SG, decltype(zero)::value, U, D>;
+    hipLaunchKernelGGL(kernel, dim3(p.groups * p.S), dim3(64 * p.W), p.lds, a.stream, k);
+    return 0;
   });
+  if (p.S > 1)
+    for (int l = 0; l < a.L; l++) {
+      const size_t count = (size_t)B * a.m[l];
+      hipLaunchKernelGGL(q4_join_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, a.stream,
+                         static_cast<const float*>(k.layer[l].out), p.S, k.part_split, count, y[l], a.y_dtype);
+    }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -609,8 +877,16 @@ Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype) {
 }
 
 size_t q4_workspace(const int* m, int L, int n, int B, int x_dtype) {
-  if (B <= Q4_DEC_MAX) return 0;
+  const int P = x_dtype == 0 ? 2 : 1;
   size_t need = 0;
+  if (B <= Q4_DEC_MAX) {  // chunks of 16 rows and one of the rest, one after another
+    if (B >= 16) need = q4_dec_plan(m, L, n, 16, P).part;
+    if (B % 16) {
+      const size_t rest = q4_dec_plan(m, L, n, B % 16, P).part;
+      need = rest > need ? rest : need;
+    }
+    return need;
+  }
   for (int l = 0; l < L; l++) {
     const size_t b = q4_gemm_plan(m[l], n, B, x_dtype).bytes;
     need = b > need ? b : need;
@@ -635,9 +911,8 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
   k.S = p.S;
   k.y = p.S > 1 ? static_cast<void*>(a.ws + p.off_part) : a.y[l];
   if (image) {
-    const int xvec = a.n % 8 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0;
     hipLaunchKernelGGL((q4_rows_kernel<XT>), dim3(a.B), dim3(256), 0, a.stream, static_cast<const XT*>(a.x), a.n,
-                       k.KT * 128, xvec, reinterpret_cast<_Float16*>(a.ws + p.off_hi),
+                       k.KT * 128, reinterpret_cast<_Float16*>(a.ws + p.off_hi),
                        reinterpret_cast<_Float16*>(a.ws + p.off_lo), reinterpret_cast<float*>(a.ws + p.off_fac));
   }
   const long long tiles = (long long)ceil_div(k.m, QM) * ceil_div(k.B, QB) * k.S;
@@ -651,7 +926,7 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
   if (p.S > 1) {
     const size_t count = (size_t)a.B * a.m[l];
     hipLaunchKernelGGL(q4_join_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, a.stream,
-                       reinterpret_cast<const float*>(a.ws + p.off_part), p.S, count, a.y[l], a.y_dtype);
+                       reinterpret_cast<const float*>(a.ws + p.off_part), p.S, count, count, a.y[l], a.y_dtype);
   }
   return hipGetLastError();
 }
@@ -680,12 +955,12 @@ hipError_t q4_pack(const Q4Layout& lay, int m, int n, int group, int scale_bytes
                      reinterpret_cast<uint32_t*>(blob + lay.off_codes), bad);
   if (scale_bytes == 2)
     hipLaunchKernelGGL((q4_pack_groups_kernel<uint16_t>), ge, dim3(256), 0, st, static_cast<const uint16_t*>(s), m, ng,
-                       KT, SG, entries, reinterpret_cast<uint16_t*>(blob + lay.off_scales), 0, bad);
+                       KT, SG, 4, entries, reinterpret_cast<uint16_t*>(blob + lay.off_scales), 0, bad);
   else
     hipLaunchKernelGGL((q4_pack_groups_kernel<uint32_t>), ge, dim3(256), 0, st, static_cast<const uint32_t*>(s), m, ng,
-                       KT, SG, entries, reinterpret_cast<uint32_t*>(blob + lay.off_scales), 0, bad);
+                       KT, SG, 4, entries, reinterpret_cast<uint32_t*>(blob + lay.off_scales), 0, bad);
   if (z)
-    hipLaunchKernelGGL((q4_pack_groups_kernel<uint8_t>), ge, dim3(256), 0, st, z, m, ng, KT, SG, entries,
+    hipLaunchKernelGGL((q4_pack_groups_kernel<uint8_t>), ge, dim3(256), 0, st, z, m, ng, KT, SG, 1, entries,
                        blob + lay.off_zeros, 15, bad);
   return hipGetLastError();
 }

@@ -89,13 +89,14 @@ def test_blob_as_documented():
                         i = 16 * rt + (lane & 15)
                         j = 128 * kt + 32 * t + 8 * (lane >> 4) + (2 * p if p < 4 else 2 * (p - 4) + 1)
                         assert (w >> (4 * p)) & 15 == (q[i, j] if i < m and j < n else 0)
-    sc = blob[int(off_scales):int(off_scales) + 3 * KT * SG * 32].view(np.float16).reshape(3, KT * SG, 16)
-    zz = blob[int(off_zeros):int(off_zeros) + 3 * KT * SG * 16].reshape(3, KT * SG, 16)
+    sc = blob[int(off_scales):int(off_scales) + 3 * KT * SG * 32].view(np.float16).reshape(3, KT, 4, SG, 4)
+    zz = blob[int(off_zeros):int(off_zeros) + 3 * KT * SG * 16].reshape(3, KT, 16, SG)
     for i in range(48):
         for g in range(KT * SG):
             inside = i < m and g < s.shape[1]
-            assert sc[i // 16, g, i % 16] == (s[i, g].numpy() if inside else 0)
-            assert zz[i // 16, g, i % 16] == (z[i, g] if inside else 0)
+            rt, r, kt, gg = i // 16, i % 16, g // SG, g % SG
+            assert sc[rt, kt, r // 4, gg, r % 4] == (s[i, g].numpy() if inside else 0)
+            assert zz[rt, kt, r, gg] == (z[i, g] if inside else 0)
 
 
 @pytest.mark.parametrize("where", ["code", "zero"])
@@ -194,6 +195,16 @@ def test_infinities_and_nan_stay_in_their_row(B, xd, value):
     w = Q.weight(q, f64(s), z, 64)[:, 299]
     some = torch.from_numpy(w != 0)
     assert torch.equal(y[1].cpu()[some], torch.from_numpy(np.sign(w) * value)[some].float())
+
+
+def test_small_scales():
+    """fp16 scales below its normal numbers keep their value."""
+    q, s, z, x = make(40, 300, 3, 64, True, "f16", "bf16")
+    s = (s.float() * 2.0 ** -20).half()
+    assert bool((s.abs() < 2.0 ** -14).all()) and bool((s != 0).any())
+    for B in (3, 70):
+        xx = x[:1].expand(B, -1).contiguous()
+        check(nq.q4_linear(xx.to(DEV), pack(q, s, z, 64), out_dtype=torch.float32), xx, q, s, z, 64)
 
 
 def test_zero_rows_and_zero_scales():
