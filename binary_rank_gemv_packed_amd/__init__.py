@@ -26,6 +26,7 @@ NQ_NORM_POST, NQ_NORM_PRE, NQ_NORM_MAX_DIM = 1, 2, 32768  # block norms (include
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "valu": 3, "decode": 4}
 
 _DT = {torch.float32: NQ_F32, torch.float16: NQ_F16, torch.bfloat16: NQ_BF16}
+_ACT = (torch.bfloat16, torch.float32)  # of activations
 
 
 class NQError(RuntimeError):
@@ -121,11 +122,23 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _here(device: torch.device, stream):
+    """The raw current stream, where a call needs no more than that: no stream
+    given and `device` current (else None; 0 is the default stream).  torch's own
+    raw form costs 0.1 us, building a Stream object to ask it 2.7 us, a third of a
+    small launch."""
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(index)
+    return None
+
+
 def _on_stream(device: torch.device, stream, call):
     """call(raw stream) with `device` current: on the given stream, else on the
     device's current one.  What call allocates belongs to that stream."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+    raw = _here(device, stream)
+    if raw is not None:
+        return call(raw)
     with torch.cuda.device(device):
         s = stream if stream is not None else torch.cuda.current_stream()
         if s.device != device:
@@ -414,15 +427,9 @@ class Q4Layer:
 
     def __init__(self, m: int, n: int, group: int, scale_dtype: torch.dtype, zeros: bool, blob: torch.Tensor):
         self.m, self.n, self.group, self.scale_dtype, self.zeros, self.blob = m, n, group, scale_dtype, zeros, blob
+        self.device = blob.device
         self.c = nq_q4_layer(m, n, group, _DT[scale_dtype], int(zeros), blob.data_ptr())
-
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
-
-    @property
-    def device(self):
-        return self.blob.device
+        self.ref = ctypes.byref(self.c)
 
 
 class Q4Group:
@@ -498,20 +505,22 @@ def new_q4_workspace(layer, B: int) -> torch.Tensor:
 
 
 def _q4_batch(x: torch.Tensor, n: int, device) -> int:
-    if x.dtype not in (torch.bfloat16, torch.float32) or x.device != device or not x.is_contiguous() or \
-            x.dim() not in (1, 2) or x.shape[-1] != n:
+    shape = x.shape
+    if x.dtype not in _ACT or x.device != device or not x.is_contiguous() or len(shape) not in (1, 2) or \
+            shape[-1] != n:
         raise NQError(NQ_ERR_INVALID_ARG, f"x must be contiguous bf16 or fp32 of shape (B, {n}) or ({n},) on {device}")
-    return x.shape[0] if x.dim() == 2 else 1
+    return shape[0] if len(shape) == 2 else 1
 
 
 def _q4_output(x: torch.Tensor, B: int, y: torch.Tensor, m: int, dtype: torch.dtype) -> None:
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype not in _ACT:
         raise NQError(NQ_ERR_INVALID_ARG, "y must be bf16 or fp32")
     _gpu_tensor(y, "y", dtype, (B, m) if x.dim() == 2 else (m,), x.device)
 
 
 def _q4_scratch(workspace: torch.Tensor, device) -> None:
-    _gpu_tensor(workspace, "the workspace", torch.uint8, (workspace.numel(),), device)
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise NQError(NQ_ERR_INVALID_ARG, f"the workspace must be a contiguous uint8 tensor on {device}")
 
 
 def q4_linear_into(x: torch.Tensor, layer: Q4Layer, y: torch.Tensor, workspace: torch.Tensor,
@@ -519,10 +528,11 @@ def q4_linear_into(x: torch.Tensor, layer: Q4Layer, y: torch.Tensor, workspace: 
     """y = x W^T into caller buffers, x (B, n) or (n,) bf16 or fp32, y (B, m) or
     (m,); enqueues on the stream and returns without synchronising (safe to
     capture in a graph)."""
-    B = _q4_batch(x, layer.n, layer.device)
+    device = layer.device
+    B = _q4_batch(x, layer.n, device)
     _q4_output(x, B, y, layer.m, y.dtype)
-    _q4_scratch(workspace, layer.device)
-    _on_stream(layer.device, stream, lambda s: _check(lib().nq_q4_linear_fwd(
+    _q4_scratch(workspace, device)
+    _on_stream(device, stream, lambda s: _check(lib().nq_q4_linear_fwd(
         layer.ref, x.data_ptr(), _DT[x.dtype], y.data_ptr(), _DT[y.dtype], B, workspace.data_ptr(),
         workspace.numel(), s)))
     return y
@@ -601,12 +611,10 @@ class BlockNorm:
         self.c = nq_block_norm(d, NQ_NORM_POST * bool(post) | NQ_NORM_PRE * bool(pre), _DT[act_dtype],
                                _DT[self.res_dtype], _DT[dtype], eps, res_scale, block_scale, weight_offset,
                                ptr(w_post), ptr(w_pre), ptr(gate))
+        self.ref = ctypes.byref(self.c)
 
-    @property
-    def ref(self):
-        return ctypes.byref(self.c)
-
-    def check(self, t, name, dtype, shape, device):
+    @staticmethod
+    def check(t, name, dtype, shape, device):
         if t is not None:
             _gpu_tensor(t, name, dtype, shape, device)
             return t.data_ptr()
@@ -617,7 +625,8 @@ def _norm_rows(h: torch.Tensor, norm: BlockNorm):
     if h.dim() != 2 or not h.is_cuda or (norm.device is not None and h.device != norm.device):
         raise NQError(NQ_ERR_INVALID_ARG, f"the residual stream must be a (rows, {norm.d}) GPU tensor on the weights' "
                                           "device")
-    return h.shape[0], torch.Size((h.shape[0], norm.d))
+    rows = h.shape[0]
+    return rows, (rows, norm.d)
 
 
 def block_norm(h: torch.Tensor, y: torch.Tensor | None, norm: BlockNorm, gate: torch.Tensor | None = None,

@@ -604,7 +604,7 @@ constexpr int QM = 128, QB = 128;  // rows of W and of x per workgroup
 // from memory straight to shared memory one step ahead, the codes of the wave's
 // four row tiles to registers one step ahead.
 template <typename ST, int SG, bool ZERO, int P>
-__global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
+__global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel(Q4GemmArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   _Float16* lds = reinterpret_cast<_Float16*>(smem);  // [2][P][QB][128]
   const int lane = threadIdx.x & 63;
@@ -629,16 +629,32 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
   // x tile: 128 rows x 16 pieces of 16 bytes; piece c of row b lies at place
   // c ^ (b & 15) of the row (see the decode kernel), so the place is fixed by the
   // thread and the column it reads from by the exchange
-  auto stage = [&](int kt, int buf) {
+  h8 xr[P][8];
+  auto fetch = [&](int kt) {
 #pragma unroll
     for (int p = 0; p < P; p++)
 #pragma unroll
       for (int c = 0; c < 8; c++) {
         const int id = c * 256 + threadIdx.x, row = id >> 4, col = ((id & 15) ^ (row & 15)) * 8;
         const int b = min(b0 + row, a.B - 1);
-        const h8 v = *reinterpret_cast<const h8*>(a.img[p] + (size_t)b * Kpad + kt * 128 + col);
-        *reinterpret_cast<h8*>(lds + ((size_t)(buf * P + p) * QB * 16 + id) * 8) = v;
+        xr[p][c] = *reinterpret_cast<const h8*>(a.img[p] + (size_t)b * Kpad + kt * 128 + col);
       }
+  };
+  auto keep = [&](int buf) {
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+      for (int c = 0; c < 8; c++)
+        *reinterpret_cast<h8*>(lds + ((size_t)(buf * P + p) * QB * 16 + c * 256 + threadIdx.x) * 8) = xr[p][c];
+  };
+  Q4Tile<ST, SG, ZERO> w[4], wn[4];
+  auto codes_of = [&](int kt) {
+#pragma unroll
+    for (int r = 0; r < 4; r++) {
+      wn[r].w = reinterpret_cast<const uint4*>(codes + (row_tile[r] + kt) * 1024)[lane];
+      wn[r].sc.load(scales, row_tile[r] + kt, lane);
+      wn[r].z.load(zeros, row_tile[r] + kt, lane);
+    }
   };
 
   v4f acc[4][4];
@@ -648,18 +664,18 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
     for (int c = 0; c < 4; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
   const Q4Magic magic;
-  if (kbeg < kend) stage(kbeg, 0);
+  if (kbeg < kend) {
+    fetch(kbeg);
+    codes_of(kbeg);
+    keep(0);
+  }
   __syncthreads();
   for (int kt = kbeg; kt < kend; kt++) {
-    const int buf = (kt - kbeg) & 1;
-    Q4Tile<ST, SG, ZERO> w[4];
+    const int buf = (kt - kbeg) & 1, next = min(kt + 1, kend - 1);
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-      w[r].w = reinterpret_cast<const uint4*>(codes + (row_tile[r] + kt) * 1024)[lane];
-      w[r].sc.load(scales, row_tile[r] + kt, lane);
-      w[r].z.load(zeros, row_tile[r] + kt, lane);
-    }
-    if (kt + 1 < kend) stage(kt + 1, buf ^ 1);
+    for (int r = 0; r < 4; r++) w[r] = wn[r];
+    codes_of(next);
+    fetch(next);
 #pragma unroll
     for (int g = 0; g < SG; g++) {
       v4f d[4][4];
@@ -698,6 +714,7 @@ __global__ void __launch_bounds__(256) q4_gemm_kernel(Q4GemmArgs a) {
           for (int v = 0; v < 4; v++) acc[r][c][v] = fmaf(w[r].sc.get(g, v), d[r][c][v], acc[r][c][v]);
       }
     }
+    keep(buf ^ 1);
     __syncthreads();
   }
 
@@ -769,7 +786,7 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
     out += (size_t)B * m[l];
   }
   const size_t per_tile = (size_t)B * (256 * P + 4);  // of the image of x
-  p.shared = per_tile * KT <= 112 * 1024;
+  p.shared = per_tile * KT <= 128 * 1024;
   if (p.shared) {
     // the whole row of x fits: the waves of a workgroup share each row tile, four
     // column tiles a wave where there are as many
