@@ -604,9 +604,9 @@ constexpr int QM = 128, QB = 128;  // rows of W and of x per workgroup
 // from memory straight to shared memory one step ahead, the codes of the wave's
 // four row tiles to registers one step ahead.
 template <typename ST, int SG, bool ZERO, int P>
-__global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel(Q4GemmArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  _Float16* lds = reinterpret_cast<_Float16*>(smem);  // [2][P][QB][128]
+__global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q4_gemm_kernel(Q4GemmArgs a) {
+  // two arrays of their own, so that reads of one do not wait for writes to the other
+  __shared__ __align__(16) _Float16 lds0[P * QB * 128], lds1[P * QB * 128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int MB = ceil_div(a.m, QM), BB = ceil_div(a.B, QB);
@@ -629,23 +629,19 @@ __global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel
   // x tile: 128 rows x 16 pieces of 16 bytes; piece c of row b lies at place
   // c ^ (b & 15) of the row (see the decode kernel), so the place is fixed by the
   // thread and the column it reads from by the exchange
-  h8 xr[P][8];
-  auto fetch = [&](int kt) {
+  auto fetch = [&](int kt, _Float16* to) {
 #pragma unroll
     for (int p = 0; p < P; p++)
 #pragma unroll
       for (int c = 0; c < 8; c++) {
         const int id = c * 256 + threadIdx.x, row = id >> 4, col = ((id & 15) ^ (row & 15)) * 8;
         const int b = min(b0 + row, a.B - 1);
-        xr[p][c] = *reinterpret_cast<const h8*>(a.img[p] + (size_t)b * Kpad + kt * 128 + col);
+        // 16 bytes a lane straight to shared memory, a wavefront's 64 in a row
+        __builtin_amdgcn_global_load_lds(
+            reinterpret_cast<const __attribute__((address_space(1))) void*>(
+                reinterpret_cast<uintptr_t>(a.img[p] + (size_t)b * Kpad + kt * 128 + col)),
+            (__attribute__((address_space(3))) void*)(to + (p * QB * 16 + c * 256 + wave * 64) * 8), 16, 0, 0);
       }
-  };
-  auto keep = [&](int buf) {
-#pragma unroll
-    for (int p = 0; p < P; p++)
-#pragma unroll
-      for (int c = 0; c < 8; c++)
-        *reinterpret_cast<h8*>(lds + ((size_t)(buf * P + p) * QB * 16 + c * 256 + threadIdx.x) * 8) = xr[p][c];
   };
   Q4Tile<ST, SG, ZERO> w[4], wn[4];
   auto codes_of = [&](int kt) {
@@ -664,18 +660,16 @@ __global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel
     for (int c = 0; c < 4; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
   const Q4Magic magic;
-  if (kbeg < kend) {
-    fetch(kbeg);
-    codes_of(kbeg);
-    keep(0);
-  }
-  __syncthreads();
-  for (int kt = kbeg; kt < kend; kt++) {
-    const int buf = (kt - kbeg) & 1, next = min(kt + 1, kend - 1);
+  // one column tile: multiplies what `from` and wn hold while the next tile comes
+  // to `to` and wn.  The reads stay in front of the products (the compiler would
+  // move them to where their results are used, and wait there).
+  auto step = [&](int kt, const _Float16* from, _Float16* to) {
+    const int next = min(kt + 1, kend - 1);
 #pragma unroll
     for (int r = 0; r < 4; r++) w[r] = wn[r];
     codes_of(next);
-    fetch(next);
+    fetch(next, to);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < SG; g++) {
       v4f d[4][4];
@@ -694,8 +688,8 @@ __global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             const int row = wb + 16 * c + (lane & 15);
-            bv[p][c] = *reinterpret_cast<const h8*>(
-                lds + ((size_t)(buf * P + p) * QB * 16 + row * 16 + ((4 * s + (lane >> 4)) ^ (row & 15))) * 8);
+            bv[p][c] =
+                *reinterpret_cast<const h8*>(from + (p * QB * 16 + row * 16 + ((4 * s + (lane >> 4)) ^ (row & 15))) * 8);
           }
 #pragma unroll
         for (int r = 0; r < 4; r++) {
@@ -713,9 +707,20 @@ __global__ void __launch_bounds__(256, SG == 1 && P == 1 ? 2 : 1) q4_gemm_kernel
 #pragma unroll
           for (int v = 0; v < 4; v++) acc[r][c][v] = fmaf(w[r].sc.get(g, v), d[r][c][v], acc[r][c][v]);
       }
+      if (SG > 1) __builtin_amdgcn_sched_barrier(0);  // one group's sums at a time
     }
-    keep(buf ^ 1);
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the next tile has come
     __syncthreads();
+  };
+  if (kbeg < kend) {
+    codes_of(kbeg);
+    fetch(kbeg, lds0);
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+    for (int kt = kbeg; kt < kend; kt += 2) {
+      step(kt, lds0, lds1);
+      if (kt + 1 < kend) step(kt + 1, lds1, lds0);
+    }
   }
 
 #pragma unroll
@@ -937,7 +942,7 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
   q4_dispatch(a.scale_dtype, a.group, a.zeros, [&](auto st, auto sg, auto zero) {
     using ST = decltype(st);
     auto kernel = q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 2 * P * QB * 256, a.stream, k);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, a.stream, k);
     return 0;
   });
   if (p.S > 1) {
