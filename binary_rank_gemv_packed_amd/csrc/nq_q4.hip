@@ -595,6 +595,7 @@ struct Q4GemmArgs {
   const float* fac;
   void* y;      // S == 1: the output; else fp32 partial sums, [S][B][m]
   int m, n, B, KT, ydt, S;
+  int quads;    // m a multiple of 4 and y aligned to four values
 };
 
 constexpr int QM = 128, QB = 128;  // rows of W and of x per workgroup
@@ -723,20 +724,34 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
     }
   }
 
+  // a lane's four rows of W lie side by side in y: one store where m lets it
+  const int odt = a.S > 1 ? 0 : a.ydt;
+  const size_t first = a.S > 1 ? (size_t)split * a.B * a.m : 0;
 #pragma unroll
   for (int c = 0; c < 4; c++) {
     const int b = b0 + wb + 16 * c + (lane & 15);
     if (b >= a.B) continue;
     const float f = a.fac[b];
 #pragma unroll
-    for (int r = 0; r < 4; r++)
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        const int i = i0 + wm + 16 * r + 4 * (lane >> 4) + v;
+    for (int r = 0; r < 4; r++) {
+      const int i = i0 + wm + 16 * r + 4 * (lane >> 4);
+      const size_t at = first + (size_t)b * a.m + i;
+      const v4f v = acc[r][c] * f;
+      if (a.quads) {
         if (i >= a.m) continue;
-        if (a.S > 1) reinterpret_cast<float*>(a.y)[((size_t)split * a.B + b) * a.m + i] = acc[r][c][v] * f;
-        else q4_store(a.y, a.ydt, (size_t)b * a.m + i, acc[r][c][v] * f);
+        if (odt == 0) {
+          *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + at) = v;
+        } else {
+          const uint32_t lo = (uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+          const uint32_t hi = (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16;
+          *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + at) = uint2{lo, hi};
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          if (i + k < a.m) q4_store(a.y, odt, at + k, v[k]);
       }
+    }
   }
 }
 
@@ -932,6 +947,7 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
   k.ydt = a.y_dtype;
   k.S = p.S;
   k.y = p.S > 1 ? static_cast<void*>(a.ws + p.off_part) : a.y[l];
+  k.quads = k.m % 4 == 0 && reinterpret_cast<uintptr_t>(k.y) % 16 == 0;
   if (image) {
     hipLaunchKernelGGL((q4_rows_kernel<XT>), dim3(a.B), dim3(256), 0, a.stream, static_cast<const XT*>(a.x), a.n,
                        k.KT * 128, reinterpret_cast<_Float16*>(a.ws + p.off_hi),
