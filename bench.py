@@ -19,14 +19,15 @@ on.  After the timed region one layer of every distinct shape of block 0 is
 checked against the fp64 oracle on the host (`parity`).  Further sections of
 the same line: `read_probe` (achievable read rates), `prefill` (2048-token
 GEMMs, MFMA utilisation), `initializer` (one ADMM step on a 7B shape),
-`variants` (transposed product and rank-l envelope on a 70B shape) and
+`variants` (transposed product and rank-l envelope on a 70B shape), `int4` (the
+chain with the norms between its blocks, on 4-bit and on binary linears) and
 `cpu_baseline` (the fp64 oracle on the host cores).
 
   python bench.py [--steps K --warmup W]           70B decode chain (the metric)
   python bench.py --batch B                        the same chain at batch B (B > 4 in passes of four rows)
   python bench.py --suite 7b --out FILE            7B shapes, B in {1,2,4,8,16}, 0.55/0.8/1.0 bpw:
                                                    per-shape GB/s over >= 1 GiB of rotating layer copies
-  python bench.py --initializer-only | --variants-only
+  python bench.py --initializer-only | --variants-only | --int4-only
 """
 from __future__ import annotations
 
@@ -67,6 +68,8 @@ def parse():
     ap.add_argument("--no-variants", action="store_true", help="skip the transposed / envelope section")
     ap.add_argument("--variants-only", action="store_true", help="run only the transposed / envelope section")
     ap.add_argument("--initializer-only", action="store_true", help="run only the ADMM initialiser section")
+    ap.add_argument("--no-int4", action="store_true", help="skip the 4-bit chain section")
+    ap.add_argument("--int4-only", action="store_true", help="run only the 4-bit chain section")
     ap.add_argument("--prefill-only", action="store_true", help="run only the 2048-token prefill section")
     ap.add_argument("--suite", default=None, choices=["7b"])
     ap.add_argument("--out", default=None)
@@ -605,6 +608,8 @@ def run_decode70b(args):
         out["initializer"] = run_initializer(dev)
     if not args.no_variants:
         out["variants"] = run_variants(dev)
+    if not args.no_int4:
+        out["int4"] = run_int4(dev)
     if not args.no_cpu_baseline:
         log("[bench] timing the CPU oracle baseline ...")
         out["cpu_baseline"] = cpu_baseline(spec, B)
@@ -703,6 +708,89 @@ def run_variants(dev, copies=6, calls=48, bpw=0.8):
             out[f"envelope_l{env}"] = {"unsupported": str(e)}
             log(f"[bench] envelope_l{env}: {e}")
     del layers, tlayers
+    torch.cuda.empty_cache()
+    return out
+
+
+# ------------------------------------------------------------------ 4-bit linears and block norms
+def run_int4(dev, distinct=8, nblocks=80, bpw=0.8, group=128):
+    """One token through 70B-shaped blocks with the norms between them, on linears
+    of 4 bits (groups of `group` columns, fp16 scales) and on binary linears at
+    `bpw` bits: per block q+k+v on the normed stream, o, post norm + residual sum
+    + pre norm, gate+up, down, and the same norms again (no attention or
+    activation: o reads q's output, down gate's).  `distinct` blocks of random
+    weights (beyond the caches) take turns; one HIP graph of `nblocks` blocks."""
+    import torch
+    import binary_rank_gemv_packed_amd as nq
+    import synth
+    shapes = synth.LLAMA70B
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(20260207)
+
+    def four_bit(name):
+        m, n = shapes[name]
+        codes = torch.randint(0, 16, (m, n), generator=gen, device=dev, dtype=torch.uint8)
+        scales = ((torch.rand(m, -(-n // group), generator=gen, device=dev) + 0.5) * 0.2 / n ** 0.5).half()
+        return nq.q4_pack(codes, scales, group=group)
+
+    def binary(name, seed):
+        m, n = shapes[name]
+        return make_layer_gpu(m, n, nq.rank_for_bits(m, n, bpw, 16), 1, seed, dev)[0]
+
+    d = shapes["q"][1]
+    weight = lambda: (1 + 0.1 * torch.randn(d, generator=gen, device=dev)).to(torch.bfloat16)  # noqa: E731
+    norm = nq.BlockNorm(d, w_post=weight(), w_pre=weight())
+    stream = torch.cuda.Stream()
+    out = {"workload": f"{nblocks} llama2-70b-shaped blocks with block norms, one token, bf16, "
+                       f"{distinct} distinct blocks", "group": group, "bits_per_weight": bpw}
+    blocks, weights = {}, {}
+    for kind in ("int4", "binary"):
+        blocks[kind] = []
+        for b in range(distinct):
+            L = {name: four_bit(name) if kind == "int4" else binary(name, 7000 + 10 * b + i)
+                 for i, name in enumerate(synth.LAYER_ORDER)}
+            blocks[kind].append(L)
+        weights[kind] = sum(l.blob.numel() for l in blocks[kind][0].values())
+    h = torch.randn(1, d, generator=gen, device=dev).to(torch.bfloat16)
+
+    def chain(kind):
+        if kind == "int4":
+            groups = [(nq.Q4Group([L[k] for k in "qkv"]), L["o"], nq.Q4Group([L["gate"], L["up"]]), L["down"])
+                      for L in blocks[kind]]
+            fan, one = nq.q4_linear_group_into, nq.q4_linear_into
+            ws = torch.empty(max(nq.q4_workspace_bytes(u, 1) for g in groups for u in g) + 256, dtype=torch.uint8,
+                             device=dev)
+        else:
+            groups = [([L[k] for k in "qkv"], L["o"], [L["gate"], L["up"]], L["down"]) for L in blocks[kind]]
+            fan, one = nq.linear_group_into, nq.linear_into
+            need = [nq.workspace_bytes_group(u, 1) if isinstance(u, list) else nq.workspace_bytes(u, 1)
+                    for u in groups[0]]
+            ws = torch.empty(max(need), dtype=torch.uint8, device=dev)
+        new = lambda *names: [torch.empty(1, shapes[k][0], device=dev, dtype=torch.bfloat16) for k in names]  # noqa: E731
+        qkv, (o,), wide, (down,) = new("q", "k", "v"), new("o"), new("gate", "up"), new("down")
+
+        def step():
+            s, x = nq.block_norm(h, None, norm)
+            for b in range(nblocks):
+                fused_qkv, lo, fused_wide, ld = groups[b % distinct]
+                fan(x, fused_qkv, qkv, ws)
+                one(qkv[0], lo, o, ws)
+                s, x = nq.block_norm(s, o, norm)
+                fan(x, fused_wide, wide, ws)
+                one(wide[0], ld, down, ws)
+                s, x = nq.block_norm(s, down, norm)
+            return x
+        return step
+
+    for kind in ("int4", "binary"):
+        ms, _ = time_graph(torch, stream, chain(kind), 3, 10)
+        out[kind] = {"ms_per_token": round(ms, 4), "tokens_per_s": round(1e3 / ms, 2),
+                     "weight_bytes_per_block": weights[kind],
+                     "gbs": round(weights[kind] * nblocks / (ms * 1e-3) / 1e9, 1)}
+        log(f"[bench] {kind} chain with norms: {ms:.3f} ms per token, {out[kind]['gbs']} GB/s of weights")
+    out["binary_speedup"] = round(out["int4"]["ms_per_token"] / out["binary"]["ms_per_token"], 3)
+    out["binary_weight_ratio"] = round(weights["int4"] / weights["binary"], 3)
+    del blocks
     torch.cuda.empty_cache()
     return out
 
@@ -951,6 +1039,8 @@ def main():
         print(json.dumps({"initializer": run_initializer("cuda:0")}), flush=True)
     elif args.variants_only:
         print(json.dumps({"variants": run_variants("cuda:0")}), flush=True)
+    elif args.int4_only:
+        print(json.dumps({"int4": run_int4("cuda:0")}), flush=True)
     elif args.prefill_only:
         print(json.dumps({"prefill": run_prefill70b("cuda:0")}), flush=True)
     else:
