@@ -174,7 +174,7 @@ hipError_t launch_balance(float* s1, float* g, float* s2, int m, int n, int r, h
 
 // Linears with 4-bit weights (nq_q4.hip): L <= GROUP_MAX layers of one width,
 // group, scale type and kind of zero point that read the same x.
-constexpr int Q4_DEC_MAX = 64;  // rows of x that run on the decode kernel, 16 at a time
+constexpr int Q4_DEC_MAX = 16;  // rows of x that the decode kernel takes (columns of its MFMA)
 struct Q4Args {
   int L, n, B;
   int m[GROUP_MAX];
@@ -188,7 +188,8 @@ struct Q4Args {
   hipStream_t stream;
 };
 struct Q4GemmPlan {
-  int S;  // K splits
+  int S;   // K splits
+  int NC;  // rows of x per workgroup, in 32
   size_t off_hi, off_lo, off_fac, off_part, bytes;
 };
 struct Q4Layout;

@@ -598,14 +598,17 @@ struct Q4GemmArgs {
   int quads;    // m a multiple of 4 and y aligned to four values
 };
 
-constexpr int QM = 128, QB = 128;  // rows of W and of x per workgroup
+constexpr int QM = 128;  // rows of W per workgroup
+constexpr int q4_gemm_cols(int NC) { return 32 * NC; }  // rows of x per workgroup
 
-// One workgroup of four waves: 128 rows of W times 128 rows of x, a wave 64 x 64
-// as 4 x 4 MFMA tiles.  A K step is one column tile (128 columns): its x goes
+// One workgroup of four waves: 128 rows of W times 128 rows of x (64 for NC = 2:
+// batches of up to 64), a wave 64 x 64 as 4 x 4 MFMA tiles (4 x NC).  A K step is one column tile (128 columns): its x goes
 // from memory straight to shared memory one step ahead, the codes of the wave's
 // four row tiles to registers one step ahead.
-template <typename ST, int SG, bool ZERO, int P>
-__global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q4_gemm_kernel(Q4GemmArgs a) {
+template <typename ST, int SG, bool ZERO, int P, int NC>
+__global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 4) ? 2 : 1)
+    q4_gemm_kernel(Q4GemmArgs a) {
+  constexpr int QB = q4_gemm_cols(NC);
   // two arrays of their own, so that reads of one do not wait for writes to the other
   __shared__ __align__(16) _Float16 lds0[P * QB * 128], lds1[P * QB * 128];
   const int lane = threadIdx.x & 63;
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
   const int KT = a.KT, Kpad = KT * 128, RT = ceil_div(a.m, 16);
   const int per_split = ceil_div(KT, a.S), kbeg = split * per_split, kend = min(KT, kbeg + per_split);
   const Q4Layout lay = q4_layout(a.m, a.n, 128 / SG, sizeof(ST), ZERO);
-  const int wm = (wave >> 1) * 64, wb = (wave & 1) * 64;
+  const int wm = (wave >> 1) * 64, wb = (wave & 1) * 16 * NC;
 
   const uint8_t *codes = a.blob + lay.off_codes, *scales = a.blob + lay.off_scales, *zeros = a.blob + lay.off_zeros;
   size_t row_tile[4];  // first tile of the wave's row tiles
@@ -634,7 +637,7 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
 #pragma unroll
     for (int p = 0; p < P; p++)
 #pragma unroll
-      for (int c = 0; c < 8; c++) {
+      for (int c = 0; c < QB / 16; c++) {
         const int id = c * 256 + threadIdx.x, row = id >> 4, col = ((id & 15) ^ (row & 15)) * 8;
         const int b = min(b0 + row, a.B - 1);
         // 16 bytes a lane straight to shared memory, a wavefront's 64 in a row
@@ -654,11 +657,11 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
     }
   };
 
-  v4f acc[4][4];
+  v4f acc[4][NC];
 #pragma unroll
   for (int r = 0; r < 4; r++)
 #pragma unroll
-    for (int c = 0; c < 4; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < NC; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
   const Q4Magic magic;
   // one column tile: multiplies what `from` and wn hold while the next tile comes
@@ -673,21 +676,21 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < SG; g++) {
-      v4f d[4][4];
+      v4f d[4][NC];
 #pragma unroll
       for (int r = 0; r < 4; r++)
 #pragma unroll
-        for (int c = 0; c < 4; c++) d[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < NC; c++) d[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
       Q4Zero zc[4];
 #pragma unroll
       for (int r = 0; r < 4; r++) zc[r] = q4_zero(w[r].z.get(g));
 #pragma unroll
       for (int s = g * 4 / SG; s < (g + 1) * 4 / SG; s++) {
-        h8 bv[P][4];
+        h8 bv[P][NC];
 #pragma unroll
         for (int p = 0; p < P; p++)
 #pragma unroll
-          for (int c = 0; c < 4; c++) {
+          for (int c = 0; c < NC; c++) {
             const int row = wb + 16 * c + (lane & 15);
             bv[p][c] =
                 *reinterpret_cast<const h8*>(from + (p * QB * 16 + row * 16 + ((4 * s + (lane >> 4)) ^ (row & 15))) * 8);
@@ -698,13 +701,13 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
 #pragma unroll
           for (int p = 0; p < P; p++)
 #pragma unroll
-            for (int c = 0; c < 4; c++) d[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bv[p][c], d[r][c], 0, 0, 0);
+            for (int c = 0; c < NC; c++) d[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bv[p][c], d[r][c], 0, 0, 0);
         }
       }
 #pragma unroll
       for (int r = 0; r < 4; r++) {
 #pragma unroll
-        for (int c = 0; c < 4; c++)
+        for (int c = 0; c < NC; c++)
 #pragma unroll
           for (int v = 0; v < 4; v++) acc[r][c][v] = fmaf(w[r].sc.get(g, v), d[r][c][v], acc[r][c][v]);
       }
@@ -728,7 +731,7 @@ __global__ void __launch_bounds__(256, P == 1 && SG * sizeof(ST) <= 4 ? 2 : 1) q
   const int odt = a.S > 1 ? 0 : a.ydt;
   const size_t first = a.S > 1 ? (size_t)split * a.B * a.m : 0;
 #pragma unroll
-  for (int c = 0; c < 4; c++) {
+  for (int c = 0; c < NC; c++) {
     const int b = b0 + wb + 16 * c + (lane & 15);
     if (b >= a.B) continue;
     const float f = a.fac[b];
@@ -840,7 +843,8 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
 }
 
 template <typename XT>
-hipError_t dec_chunk(const Q4Args& a, int b0, int B) {
+hipError_t dec_forward(const Q4Args& a) {
+  const int B = a.B;
   constexpr int P = sizeof(XT) == 4 ? 2 : 1;
   const Q4DecPlan p = q4_dec_plan(a.m, a.L, a.n, B, P);
   Q4DecArgs k{};
@@ -853,18 +857,15 @@ hipError_t dec_chunk(const Q4Args& a, int b0, int B) {
   k.groups = p.groups;
   k.keep = p.keep;
   k.odt = p.S > 1 ? 0 : a.y_dtype;
-  const XT* x = static_cast<const XT*>(a.x) + (size_t)b0 * a.n;
-  k.x = x;
+  k.x = a.x;
   float* part = reinterpret_cast<float*>(a.ws);
-  void* y[GROUP_MAX];
   for (int l = 0; l < a.L; l++) {
     const Q4Layout lay = q4_layout(a.m[l], a.n, a.group, a.scale_dtype == 1 ? 2 : 4, a.zeros);
-    y[l] = static_cast<uint8_t*>(a.y[l]) + (size_t)b0 * a.m[l] * (a.y_dtype == 0 ? 4 : 2);
     Q4DecLayer& c = k.layer[l];
     c.codes = a.blob[l] + lay.off_codes;
     c.scales = a.blob[l] + lay.off_scales;
     c.zeros = a.blob[l] + lay.off_zeros;
-    c.out = p.S > 1 ? static_cast<void*>(part + k.part_split) : y[l];
+    c.out = p.S > 1 ? static_cast<void*>(part + k.part_split) : a.y[l];
     c.m = a.m[l];
     k.rows += ceil_div(a.m[l], 16);
     c.rt_end = k.rows;
@@ -885,7 +886,8 @@ hipError_t dec_chunk(const Q4Args& a, int b0, int B) {
     for (int l = 0; l < a.L; l++) {
       const size_t count = (size_t)B * a.m[l];
       hipLaunchKernelGGL(q4_join_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, a.stream,
-                         static_cast<const float*>(k.layer[l].out), p.S, k.part_split, count, y[l], a.y_dtype);
+                         static_cast<const float*>(k.layer[l].out), p.S, k.part_split, count, a.y[l],
+                         a.y_dtype);
     }
   return hipGetLastError();
 }
@@ -895,9 +897,11 @@ hipError_t dec_chunk(const Q4Args& a, int b0, int B) {
 Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype) {
   Q4GemmPlan p{};
   const int KT = ceil_div(n, 128), P = x_dtype == 0 ? 2 : 1;
-  const long long tiles = (long long)ceil_div(m, QM) * ceil_div(B, QB);
+  p.NC = B <= 64 ? 2 : 4;
+  const long long tiles = (long long)ceil_div(m, QM) * ceil_div(B, q4_gemm_cols(p.NC));
+  // K splits while the tiles leave CUs idle, each of at least four steps
   int S = 1;
-  while (tiles * S < 384 && S < 8 && KT / (2 * S) >= 4) S *= 2;
+  while (tiles * S < 384 && S < 32 && KT / (2 * S) >= 4) S *= 2;
   p.S = ceil_div(KT, ceil_div(KT, S));
   size_t o = 0;
   auto take = [&](size_t bytes) {
@@ -916,14 +920,7 @@ Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype) {
 size_t q4_workspace(const int* m, int L, int n, int B, int x_dtype) {
   const int P = x_dtype == 0 ? 2 : 1;
   size_t need = 0;
-  if (B <= Q4_DEC_MAX) {  // chunks of 16 rows and one of the rest, one after another
-    if (B >= 16) need = q4_dec_plan(m, L, n, 16, P).part;
-    if (B % 16) {
-      const size_t rest = q4_dec_plan(m, L, n, B % 16, P).part;
-      need = rest > need ? rest : need;
-    }
-    return need;
-  }
+  if (B <= Q4_DEC_MAX) return q4_dec_plan(m, L, n, B, P).part;
   for (int l = 0; l < L; l++) {
     const size_t b = q4_gemm_plan(m[l], n, B, x_dtype).bytes;
     need = b > need ? b : need;
@@ -953,11 +950,12 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
                        k.KT * 128, reinterpret_cast<_Float16*>(a.ws + p.off_hi),
                        reinterpret_cast<_Float16*>(a.ws + p.off_lo), reinterpret_cast<float*>(a.ws + p.off_fac));
   }
-  const long long tiles = (long long)ceil_div(k.m, QM) * ceil_div(k.B, QB) * k.S;
+  const long long tiles = (long long)ceil_div(k.m, QM) * ceil_div(k.B, q4_gemm_cols(p.NC)) * k.S;
   const dim3 grid((unsigned)(8 * ((tiles + 7) / 8)));
   q4_dispatch(a.scale_dtype, a.group, a.zeros, [&](auto st, auto sg, auto zero) {
     using ST = decltype(st);
-    auto kernel = q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P>;
+    auto kernel = p.NC == 2 ? q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 2>
+                            : q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 4>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, a.stream, k);
     return 0;
   });
@@ -970,14 +968,8 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
 }
 
 hipError_t q4_forward(const Q4Args& a) {
+  if (a.B <= Q4_DEC_MAX) return a.x_dtype == 0 ? dec_forward<float>(a) : dec_forward<uint16_t>(a);
   hipError_t e = hipSuccess;
-  if (a.B <= Q4_DEC_MAX) {
-    for (int b0 = 0; b0 < a.B && e == hipSuccess; b0 += 16) {
-      const int B = a.B - b0 < 16 ? a.B - b0 : 16;
-      e = a.x_dtype == 0 ? dec_chunk<float>(a, b0, B) : dec_chunk<uint16_t>(a, b0, B);
-    }
-    return e;
-  }
   // the image of x lies at the same place for every layer of the group
   for (int l = 0; l < a.L && e == hipSuccess; l++)
     e = a.x_dtype == 0 ? gemm_layer<float>(a, l, l == 0) : gemm_layer<uint16_t>(a, l, l == 0);
