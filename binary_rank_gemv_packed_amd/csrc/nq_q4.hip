@@ -303,6 +303,7 @@ struct Q4DecArgs {
   int range, tpw, steps;  // column tiles of a split, of a wave; units of a wave's row tile
   int shared;             // the waves share each row tile; else each has its own
   int groups;             // workgroups of one split
+  int tw;                 // log2 of the tiles that the workgroup turns over side by side
   int keep;               // row tiles whose shared sums are kept before they are added
   int odt;                // dtype of out
   size_t part_split;      // values between the splits' partial sums
@@ -390,21 +391,34 @@ __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
   const int units = turns * a.steps;
   {
     const XT* x = reinterpret_cast<const XT*>(a.x);
-    const int j = lane & 15, pieces = (k_hi - k_lo) * B, by = blockDim.x >> 4;
+    // the workgroup's groups of sixteen lanes as TW tiles x BW rows; a group goes
+    // through rows b0, b0 + BW, ... of tiles t0, t0 + TW, ... (powers of two: a
+    // division by B would cost as much as the turning over)
+    const int j = lane & 15, g = threadIdx.x >> 4, span = k_hi - k_lo;
+    const int TW = 1 << a.tw, BW = max((int)(blockDim.x >> 4) >> a.tw, 1);
+    const int t0 = g & (TW - 1), b0 = g >> a.tw;
+    const int pieces = ceil_div(span, TW) * ceil_div(B, BW);
     Q4X<XT> raw[XN];
-    auto fetch = [&](int u0, int count) {
-#pragma unroll
-      for (int i = 0; i < XN; i++) {
-        if (i >= count) break;
-        const int u = min(u0 + i * by, pieces - 1);
-        raw[i].load(x + (size_t)(u % B) * a.n, (k_lo + u / B) * 128 + 8 * j, a.n);
+    int tf = t0, bf = b0, tt = t0, bt = b0;  // the next to fetch and to turn over
+    auto advance = [&](int& t, int& b) {
+      b += BW;
+      if (b >= B) {
+        b = b0;
+        t += TW;
       }
     };
-    auto turn_over = [&](int u0, int count) {
+    auto fetch = [&](int count) {
 #pragma unroll
       for (int i = 0; i < XN; i++) {
         if (i >= count) break;
-        const int u = u0 + i * by;
+        raw[i].load(x + (size_t)min(bf, B - 1) * a.n, (k_lo + min(tf, span - 1)) * 128 + 8 * j, a.n);
+        advance(tf, bf);
+      }
+    };
+    auto turn_over = [&](int count) {
+#pragma unroll
+      for (int i = 0; i < XN; i++) {
+        if (i >= count) break;
         uint32_t mx = row16_max(raw[i].template top<false>());
         if (mx >= 0x7f800000u) mx = row16_max(raw[i].template top<true>());
         const int e = q4_block_exp(mx);
@@ -412,24 +426,26 @@ __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
         raw[i].get(v);
         h8 hi, lo;
         q4_to_f16<P>(v, q4_exp2(e), &hi, &lo);
-        if (u >= pieces) continue;
-        const int at = (u * 16 + (j ^ (u % B & 15))) * 8;
+        const int t = tt, b = bt;
+        advance(tt, bt);
+        if (t >= span || b >= B) continue;
+        const int u = t * B + b, at = (u * 16 + (j ^ (b & 15))) * 8;
         *reinterpret_cast<h8*>(img + at) = hi;
         if (P == 2) *reinterpret_cast<h8*>(img + (size_t)KR * B * 128 + at) = lo;
         if (j == 0) xfac[u] = q4_exp2(-e);
       }
     };
-    int u0 = threadIdx.x >> 4, left = ceil_div(pieces, by);
-    for (; left > XN; left -= XN, u0 += XN * by) {
-      fetch(u0, XN);
-      turn_over(u0, XN);
+    int left = pieces;
+    for (; left > XN; left -= XN) {
+      fetch(XN);
+      turn_over(XN);
     }
-    fetch(u0, left);
+    fetch(left);
     __builtin_amdgcn_s_barrier();
     seek();
 #pragma unroll
     for (int t = 0; t < PRE; t++) load(ring[0][t], t);
-    turn_over(u0, left);
+    turn_over(left);
   }
 #pragma unroll
   for (int t = PRE; t < U; t++) load(ring[0][t], t);
@@ -856,6 +872,7 @@ hipError_t dec_forward(const Q4Args& a) {
   k.shared = p.shared;
   k.groups = p.groups;
   k.keep = p.keep;
+  while ((1 << k.tw) < p.range && (1 << k.tw) < 4 * p.W) k.tw++;
   k.odt = p.S > 1 ? 0 : a.y_dtype;
   k.x = a.x;
   float* part = reinterpret_cast<float*>(a.ws);
