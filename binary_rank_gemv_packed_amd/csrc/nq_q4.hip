@@ -312,7 +312,7 @@ struct Q4DecArgs {
 // The codes, scales and zero points of one tile, as one lane holds them.
 template <typename ST, int SG, bool ZERO>
 struct Q4Tile {
-  uint4 w;
+  u32x4 w;
   Q4Scales<ST, SG> sc;
   Q4Zeros<SG, ZERO> z;
 };
@@ -328,7 +328,9 @@ struct Q4Tile {
 // 8 (lane >> 4) .. + 7, the second row b = lane & 15 of x and the same columns; the
 // result has row 4 (lane >> 4) + v of the tile for b = lane & 15.  Lanes with
 // b >= B repeat row B - 1 and are not stored.
-template <typename XT, typename ST, int SG, bool ZERO, int U, int D>
+// STREAM: codes that no cache will hold until the next call are read past the
+// caches' replacement (host side: q4_streams).
+template <typename XT, typename ST, int SG, bool ZERO, int U, int D, bool STREAM>
 __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
   constexpr int P = sizeof(XT) == 4 ? 2 : 1;
   constexpr int XN = 8 / P;  // pieces of x that a thread reads at a time
@@ -372,7 +374,8 @@ __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
   auto load = [&](Q4Tile<ST, SG, ZERO>& q, int t) {
     // past the run its last tile is asked for again
     const size_t tile = ask_tile + max(min(kbeg + ask_step * U + t, kend - 1), 0);
-    q.w = reinterpret_cast<const uint4*>(codes + tile * 1024)[lane];
+    const u32x4* w = reinterpret_cast<const u32x4*>(codes + tile * 1024) + lane;
+    q.w = STREAM ? __builtin_nontemporal_load(w) : *w;
     q.sc.load(scales, tile, lane);
     q.z.load(zeros, tile, lane);
   };
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
   auto codes_of = [&](int kt) {
 #pragma unroll
     for (int r = 0; r < 4; r++) {
-      wn[r].w = reinterpret_cast<const uint4*>(codes + (row_tile[r] + kt) * 1024)[lane];
+      wn[r].w = reinterpret_cast<const u32x4*>(codes + (row_tile[r] + kt) * 1024)[lane];
       wn[r].sc.load(scales, row_tile[r] + kt, lane);
       wn[r].z.load(zeros, row_tile[r] + kt, lane);
     }
@@ -825,12 +828,18 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
     out += (size_t)B * m[l];
   }
   const size_t per_tile = (size_t)B * (256 * P + 4);  // of the image of x
-  p.shared = per_tile * KT <= 128 * 1024;
+  const bool small = per_tile * KT <= 40 * 1024;
+  // a large image for few row tiles is not worth turning over whole: 1100 x 4099,
+  // 7 rows of fp32 (116 KB, 69 row tiles), 13.7 us shared, 12.0 us split
+  p.shared = per_tile * KT <= (RT < 128 ? 64 : 128) * 1024;
   if (p.shared) {
     // the whole row of x fits: the waves of a workgroup share each row tile, four
-    // column tiles a wave where there are as many
-    const int w = ceil_div(KT, 4);
-    p.W = w < 16 ? w : 16;
+    // column tiles a wave where there are as many.  A small image (one row of x, two
+    // of 8192) is turned over twice rather than once, and two workgroups of 8 waves
+    // a CU do not wait for each other: 8192 x 8192, 12.4 -> 10.9 us; with four rows
+    // of 8192 the turning over costs more, 31.5 -> 34.3 us for 32000 rows of W.
+    const int most = small ? 8 : 16, w = ceil_div(KT, 4);
+    p.W = w < most ? w : most;
     p.S = 1;
     // 16 waves a CU
     const int fill = 256 * (16 / p.W);
@@ -850,13 +859,18 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
   p.lds = per_tile * p.range;
   if (p.shared) {
     const int turns = ceil_div(RT, p.groups), each = p.W * 16 * B * 4;
-    const int fit = (int)((MAX_LDS - p.lds) / each);
+    const int fit = (int)(((small ? MAX_LDS / 2 : MAX_LDS) - p.lds) / each);  // at least 2
     p.keep = turns < fit ? turns : fit;
     p.lds += (size_t)p.keep * each;
   }
   p.part = p.S > 1 ? p.S * out * 4 : 0;
   return p;
 }
+
+// Codes of 16 MB or more are read as a stream: 8192 x 8192, 12.4 -> 11.5 us, gate and
+// up of a 70B block 53 -> 50.6 us; below, what the caches keep is worth more:
+// 4096 x 4096 (8 MB), 5.5 us against 5.9 us read as a stream.
+bool q4_streams(const Q4DecArgs& k) { return (size_t)k.rows * k.KT * 1024 >= (size_t)16 << 20; }
 
 template <typename XT>
 hipError_t dec_forward(const Q4Args& a) {
@@ -895,7 +909,8 @@ hipError_t dec_forward(const Q4Args& a) {
     // the operands
     constexpr int U = bytes == 2 ? 4 : bytes <= 8 ? 2 : 1, D = bytes == 4 || bytes == 16 ? 3 : 2;
     k.steps = ceil_div(p.tpw, U);
-    auto kernel = q4_dec_kernel<XT, ST, SG, decltype(zero)::value, U, D>;
+    constexpr bool Z = decltype(zero)::value;
+    auto kernel = q4_streams(k) ? q4_dec_kernel<XT, ST, SG, Z, U, D, true> : q4_dec_kernel<XT, ST, SG, Z, U, D, false>;
     hipLaunchKernelGGL(kernel, dim3(p.groups * p.S), dim3(64 * p.W), p.lds, a.stream, k);
     return 0;
   });
