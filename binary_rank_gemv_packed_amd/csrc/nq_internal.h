@@ -189,7 +189,7 @@ struct Q4Args {
 };
 struct Q4GemmPlan {
   int S;   // K splits
-  int NC;  // rows of x per workgroup, in 32
+  int NC;  // rows of x per workgroup, in 16
   size_t off_hi, off_lo, off_fac, off_part, bytes;
 };
 struct Q4Layout;

@@ -618,16 +618,23 @@ struct Q4GemmArgs {
 };
 
 constexpr int QM = 128;  // rows of W per workgroup
-constexpr int q4_gemm_cols(int NC) { return 32 * NC; }  // rows of x per workgroup
 
-// One workgroup of four waves: 128 rows of W times 128 rows of x (64 for NC = 2:
-// batches of up to 64), a wave 64 x 64 as 4 x 4 MFMA tiles (4 x NC).  A K step is one column tile (128 columns): its x goes
-// from memory straight to shared memory one step ahead, the codes of the wave's
-// four row tiles to registers one step ahead.
+// Waits for every read of this wave, those straight to shared memory among them;
+// no access to memory moves across.
+__device__ __forceinline__ void wait_vmem() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// One workgroup of four waves: 128 rows of W times QB = 16 NC rows of x (128, or 64
+// for batches of up to 64), a wave 32 rows of W times all of x as 2 x NC MFMA
+// tiles: no two waves expand the same codes.  (Waves of 64 x 64, which read half
+// as much from shared memory but expand every code twice: 2048 x 4096 -> 11008,
+// 215 us against 200 us; 34 x 9728 -> 8832 with groups of 32, 78 against 41 us.)
+// A K step is one column tile (128 columns): its x goes from memory straight to
+// shared memory one step ahead, the codes of the wave's two row tiles to registers
+// one step ahead.
 template <typename ST, int SG, bool ZERO, int P, int NC>
-__global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 4) ? 2 : 1)
+__global__ void __launch_bounds__(256, NC == 4 || (P == 1 && SG * sizeof(ST) <= 4) ? 2 : 1)
     q4_gemm_kernel(Q4GemmArgs a) {
-  constexpr int QB = q4_gemm_cols(NC);
+  constexpr int QB = 16 * NC;  // rows of x per workgroup
   // two arrays of their own, so that reads of one do not wait for writes to the other
   __shared__ __align__(16) _Float16 lds0[P * QB * 128], lds1[P * QB * 128];
   const int lane = threadIdx.x & 63;
@@ -643,12 +650,12 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
   const int KT = a.KT, Kpad = KT * 128, RT = ceil_div(a.m, 16);
   const int per_split = ceil_div(KT, a.S), kbeg = split * per_split, kend = min(KT, kbeg + per_split);
   const Q4Layout lay = q4_layout(a.m, a.n, 128 / SG, sizeof(ST), ZERO);
-  const int wm = (wave >> 1) * 64, wb = (wave & 1) * 16 * NC;
+  const int wm = wave * 32;
 
   const uint8_t *codes = a.blob + lay.off_codes, *scales = a.blob + lay.off_scales, *zeros = a.blob + lay.off_zeros;
-  size_t row_tile[4];  // first tile of the wave's row tiles
+  size_t row_tile[2];  // first tile of the wave's row tiles
 #pragma unroll
-  for (int r = 0; r < 4; r++) row_tile[r] = (size_t)min((i0 + wm) / 16 + r, RT - 1) * KT;
+  for (int r = 0; r < 2; r++) row_tile[r] = (size_t)min((i0 + wm) / 16 + r, RT - 1) * KT;
   // x tile: 128 rows x 16 pieces of 16 bytes; piece c of row b lies at place
   // c ^ (b & 15) of the row (see the decode kernel), so the place is fixed by the
   // thread and the column it reads from by the exchange
@@ -666,19 +673,19 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
             (__attribute__((address_space(3))) void*)(to + (p * QB * 16 + c * 256 + wave * 64) * 8), 16, 0, 0);
       }
   };
-  Q4Tile<ST, SG, ZERO> w[4], wn[4];
+  Q4Tile<ST, SG, ZERO> w[2], wn[2];
   auto codes_of = [&](int kt) {
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
+    for (int r = 0; r < 2; r++) {
       wn[r].w = reinterpret_cast<const u32x4*>(codes + (row_tile[r] + kt) * 1024)[lane];
       wn[r].sc.load(scales, row_tile[r] + kt, lane);
       wn[r].z.load(zeros, row_tile[r] + kt, lane);
     }
   };
 
-  v4f acc[4][NC];
+  v4f acc[2][NC];
 #pragma unroll
-  for (int r = 0; r < 4; r++)
+  for (int r = 0; r < 2; r++)
 #pragma unroll
     for (int c = 0; c < NC; c++) acc[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
 
@@ -689,20 +696,20 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
   auto step = [&](int kt, const _Float16* from, _Float16* to) {
     const int next = min(kt + 1, kend - 1);
 #pragma unroll
-    for (int r = 0; r < 4; r++) w[r] = wn[r];
+    for (int r = 0; r < 2; r++) w[r] = wn[r];
     codes_of(next);
     fetch(next, to);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < SG; g++) {
-      v4f d[4][NC];
+      v4f d[2][NC];
 #pragma unroll
-      for (int r = 0; r < 4; r++)
+      for (int r = 0; r < 2; r++)
 #pragma unroll
         for (int c = 0; c < NC; c++) d[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
-      Q4Zero zc[4];
+      Q4Zero zc[2];
 #pragma unroll
-      for (int r = 0; r < 4; r++) zc[r] = q4_zero(w[r].z.get(g));
+      for (int r = 0; r < 2; r++) zc[r] = q4_zero(w[r].z.get(g));
 #pragma unroll
       for (int s = g * 4 / SG; s < (g + 1) * 4 / SG; s++) {
         h8 bv[P][NC];
@@ -710,12 +717,12 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
         for (int p = 0; p < P; p++)
 #pragma unroll
           for (int c = 0; c < NC; c++) {
-            const int row = wb + 16 * c + (lane & 15);
+            const int row = 16 * c + (lane & 15);
             bv[p][c] =
                 *reinterpret_cast<const h8*>(from + (p * QB * 16 + row * 16 + ((4 * s + (lane >> 4)) ^ (row & 15))) * 8);
           }
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
+        for (int r = 0; r < 2; r++) {
           const h8 av = q4_expand(s == 0 ? w[r].w.x : s == 1 ? w[r].w.y : s == 2 ? w[r].w.z : w[r].w.w, zc[r], magic);
 #pragma unroll
           for (int p = 0; p < P; p++)
@@ -724,7 +731,7 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
         }
       }
 #pragma unroll
-      for (int r = 0; r < 4; r++) {
+      for (int r = 0; r < 2; r++) {
 #pragma unroll
         for (int c = 0; c < NC; c++)
 #pragma unroll
@@ -732,13 +739,13 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
       }
       if (SG > 1) __builtin_amdgcn_sched_barrier(0);  // one group's sums at a time
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's part of the next tile has come
+    wait_vmem();  // this wave's part of the next tile has come
     __syncthreads();
   };
   if (kbeg < kend) {
     codes_of(kbeg);
     fetch(kbeg, lds0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
+    wait_vmem();
     __syncthreads();
     for (int kt = kbeg; kt < kend; kt += 2) {
       step(kt, lds0, lds1);
@@ -751,11 +758,11 @@ __global__ void __launch_bounds__(256, NC == 2 || (P == 1 && SG * sizeof(ST) <= 
   const size_t first = a.S > 1 ? (size_t)split * a.B * a.m : 0;
 #pragma unroll
   for (int c = 0; c < NC; c++) {
-    const int b = b0 + wb + 16 * c + (lane & 15);
+    const int b = b0 + 16 * c + (lane & 15);
     if (b >= a.B) continue;
     const float f = a.fac[b];
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
+    for (int r = 0; r < 2; r++) {
       const int i = i0 + wm + 16 * r + 4 * (lane >> 4);
       const size_t at = first + (size_t)b * a.m + i;
       const v4f v = acc[r][c] * f;
@@ -929,8 +936,8 @@ hipError_t dec_forward(const Q4Args& a) {
 Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype) {
   Q4GemmPlan p{};
   const int KT = ceil_div(n, 128), P = x_dtype == 0 ? 2 : 1;
-  p.NC = B <= 64 ? 2 : 4;
-  const long long tiles = (long long)ceil_div(m, QM) * ceil_div(B, q4_gemm_cols(p.NC));
+  p.NC = B <= 64 ? 4 : 8;
+  const long long tiles = (long long)ceil_div(m, QM) * ceil_div(B, 16 * p.NC);
   // K splits while the tiles leave CUs idle, each of at least four steps
   int S = 1;
   while (tiles * S < 384 && S < 32 && KT / (2 * S) >= 4) S *= 2;
@@ -982,12 +989,12 @@ static hipError_t gemm_layer(const Q4Args& a, int l, bool image) {
                        k.KT * 128, reinterpret_cast<_Float16*>(a.ws + p.off_hi),
                        reinterpret_cast<_Float16*>(a.ws + p.off_lo), reinterpret_cast<float*>(a.ws + p.off_fac));
   }
-  const long long tiles = (long long)ceil_div(k.m, QM) * ceil_div(k.B, q4_gemm_cols(p.NC)) * k.S;
+  const long long tiles = (long long)ceil_div(k.m, QM) * ceil_div(k.B, 16 * p.NC) * k.S;
   const dim3 grid((unsigned)(8 * ((tiles + 7) / 8)));
   q4_dispatch(a.scale_dtype, a.group, a.zeros, [&](auto st, auto sg, auto zero) {
     using ST = decltype(st);
-    auto kernel = p.NC == 2 ? q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 2>
-                            : q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 4>;
+    auto kernel = p.NC == 4 ? q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 4>
+                            : q4_gemm_kernel<ST, decltype(sg)::value, decltype(zero)::value, P, 8>;
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, a.stream, k);
     return 0;
   });

@@ -145,6 +145,29 @@ def test_long_and_wide(m, n, B):
     check(nq.q4_linear(x.to(DEV), pack(q, s, z, 128), out_dtype=torch.float32), x, q, s, z, 128)
 
 
+@pytest.mark.parametrize("m,n,B,xd", [(64, 28672, 16, "bf16"), (2100, 28672, 2, "f32"), (5000, 16384, 9, "f32"),
+                                      (300, 28672, 3, "bf16"), (130, 28672, 70, "bf16"), (4100, 8192, 5, "bf16"),
+                                      (2000, 9000, 1, "bf16")])
+def test_columns_split_and_shared(m, n, B, xd):
+    """Row lengths and batches on both sides of what a workgroup holds of x."""
+    for G, zeros in ((128, True), (32, False)):
+        q, s, z, x = make(m, n, B, G, zeros, "f16", xd)
+        layer = pack(q, s, z, G)
+        need = nq.q4_workspace_bytes(layer, B)
+        ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=DEV)
+        y = torch.full((B, m), float("nan"), device=DEV)
+        check(nq.q4_linear_into(x.to(DEV), layer, y, ws), x, q, s, z, G)
+        assert bool((ws[need:] == 0xFF).all())
+
+
+def test_a_layer_twice_in_a_group():
+    q, s, z, x = make(100, 300, 4, 64, True, "f16", "bf16")
+    layer = pack(q, s, z, 64)
+    a, b, c = nq.q4_linear_group(x.to(DEV), [layer, layer, layer], out_dtype=torch.float32)
+    assert torch.equal(a, b) and torch.equal(a, c)
+    check(a, x, q, s, z, 64)
+
+
 @pytest.mark.parametrize("B", [1, 4, 16, 40, 200])
 @pytest.mark.parametrize("G", [32, 64, 128])
 @pytest.mark.parametrize("xd", ["bf16", "f32"])
