@@ -553,7 +553,8 @@ def q4_linear(x: torch.Tensor, layer: Q4Layer, out_dtype: torch.dtype | None = N
 
 def q4_linear_group_into(x: torch.Tensor, layers, ys, workspace: torch.Tensor, stream=None):
     """ys[l] = x W_l^T for 4-bit layers sharing x (a Q4Group, or a list of
-    layers); one launch for all of them up to B = 16."""
+    layers); one launch for all of them up to B = 16, and one
+    more a layer where the columns are split."""
     group = layers if isinstance(layers, Q4Group) else Q4Group(layers)
     B = _q4_batch(x, group.n, group.device)
     if len(ys) != len(group):

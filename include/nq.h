@@ -314,7 +314,9 @@ nq_status nq_q4_linear_fwd(const nq_q4_layer* L, const void* x, int32_t x_dtype,
 
 /* 1..NQ_GROUP_MAX 4-bit layers that read the same x (q, k and v; gate and up):
  * ys[l] = x W_l^T, B x m_l.  The layers share n, group, scale dtype and kind of
- * zero point (else NQ_ERR_INVALID_ARG); up to B = 16 one launch runs them all.
+ * zero point (else NQ_ERR_INVALID_ARG); up to B = 16 one launch runs them all, and one
+ * more for each layer adds partial sums where the columns are split (an x too
+ * large for shared memory, or few rows of W).
  * No ys[l] may overlap x, the workspace or another. */
 size_t nq_q4_workspace_bytes_group(const nq_q4_layer* const* layers, int32_t L, int32_t B);
 nq_status nq_q4_linear_fwd_group(const nq_q4_layer* const* layers, int32_t L, const void* x, int32_t x_dtype,

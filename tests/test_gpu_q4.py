@@ -6,7 +6,7 @@ M bounds, taken at 2^-23 each (an MFMA may truncate); fp32 x adds 2^-22 M for it
 two fp16 pieces, and parts under 2^-39 of the largest of a row are dropped.  A
 worst case of n roundings that all add up does not happen for more than a few
 terms: the bound taken is the longest chain of one element, 128 sums in a group
-(256 for two pieces), one a group and one for each of up to 16 waves or splits.
+(256 for two pieces), one a group and one for each of up to 16 waves or 32 splits.
 A bf16 output adds half a step, 2^-8 of the value."""
 import numpy as np
 import pytest
