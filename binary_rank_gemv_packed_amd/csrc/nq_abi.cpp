@@ -856,6 +856,13 @@ nq_status nq_q4_linear_fwd_group(const nq_q4_layer* const* layers, int32_t L, co
     for (int32_t k = 0; k < l; k++)
       if (spans_overlap(ys[k], (size_t)B * a.m[k] * yb, ys[l], y_bytes))
         return fail(NQ_ERR_INVALID_ARG, "outputs %d and %d overlap", k, l);
+    for (int32_t k = 0; k < L; k++) {
+      const size_t blob_bytes = q4_layout_of(layers[k]).total;
+      if (spans_overlap(a.blob[k], blob_bytes, ys[l], y_bytes))
+        return fail(NQ_ERR_INVALID_ARG, "output %d and the weights of layer %d overlap", l, k);
+      if (need && workspace && spans_overlap(a.blob[k], blob_bytes, workspace, need))
+        return fail(NQ_ERR_INVALID_ARG, "the workspace and the weights of layer %d overlap", k);
+    }
   }
   if (workspace_bytes < need)
     return fail(NQ_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);

@@ -299,7 +299,7 @@ size_t nq_q4_workspace_bytes(const nq_q4_layer* L, int32_t B);
 /* y = x W^T for a batch of B rows, any B.
  *   x : device, B x n row-major, x_dtype NQ_BF16 or NQ_F32, aligned to its element size
  *   y : device, B x m row-major, y_dtype NQ_BF16 or NQ_F32, aligned to its element
- *       size; must not overlap x or the workspace
+ *       size; must not overlap x, the workspace or the weights
  *   workspace : device, >= nq_q4_workspace_bytes(L, B), 256-byte aligned; may be
  *       NULL when that is 0
  * The products are exact or off by at most 2^-22, sums are fp32, y is rounded
@@ -317,7 +317,7 @@ nq_status nq_q4_linear_fwd(const nq_q4_layer* L, const void* x, int32_t x_dtype,
  * zero point (else NQ_ERR_INVALID_ARG); up to B = 16 one launch runs them all, and one
  * more for each layer adds partial sums where the columns are split (an x too
  * large for shared memory, or few rows of W).
- * No ys[l] may overlap x, the workspace or another. */
+ * No ys[l] may overlap x, the workspace, the weights or another. */
 size_t nq_q4_workspace_bytes_group(const nq_q4_layer* const* layers, int32_t L, int32_t B);
 nq_status nq_q4_linear_fwd_group(const nq_q4_layer* const* layers, int32_t L, const void* x, int32_t x_dtype,
                                  void* const* ys, int32_t y_dtype, int32_t B, void* workspace,

@@ -118,6 +118,21 @@ def test_q4_workspace(L):
     assert q4_fwd(L, lay, B=2048, wsb=big // 4) == WS
 
 
+def test_q4_outputs_on_the_weights(L):
+    """An output or a workspace in use that lies on a layer's packed weights."""
+    end = L.nq_q4_layer_bytes(q4().m, q4().n, q4().group, q4().scale_dtype, q4().zeros)
+    for y in (FAKE, FAKE + end - 2):
+        assert q4_fwd(L, y=y) == BAD
+        assert b"weights" in L.nq_last_error()
+    assert q4_fwd(L, B=300, ws=FAKE) == BAD
+    assert b"weights" in L.nq_last_error()
+    a, b = q4(m=64), q4(m=32, blob=FAKE + GB)
+    for ys in ((FAKE + GB, FAKE + 3 * GB), (FAKE + 3 * GB, FAKE)):  # on the other layer's
+        assert L.nq_q4_linear_fwd_group(_group([a, b]), 2, FAKE + 2 * GB, nq.NQ_BF16, (ctypes.c_void_p * 2)(*ys),
+                                        nq.NQ_BF16, 1, None, 0, None) == BAD
+        assert b"weights" in L.nq_last_error()
+
+
 def _group(layers):
     return ctypes.cast((ctypes.POINTER(nq.nq_q4_layer) * len(layers))(*[ctypes.pointer(l) for l in layers]),
                        ctypes.c_void_p)
