@@ -14,8 +14,8 @@
 // below is under 2^-39 of it.  An fp32 value is taken as two fp16 pieces, the
 // rounded value and its rounded remainder, off by at most 2^-22 of itself.  So
 // the products are exact or nearly so, the sums over a group are held by the
-// fp16 MFMA in fp32, and s times the block's power of two multiplies the group's
-// sum in fp32.  y is rounded once.
+// fp16 MFMA in fp32; s multiplies the group's sum and then the block's power of two
+// the product, both in fp32.  y is rounded once.
 #include "nq_common.h"
 #include "nq_internal.h"
 
@@ -543,9 +543,11 @@ __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
         d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bh[s], d, 0, 0, 0);
         if (P == 2) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(av, bl[s], d, 0, 0, 0);
       }
-      // f is a power of two: d f is exact
+      // The scale first, though that rounds once more: f (2^-120 .. 2^113) times d
+      // alone passes fp32 where x is large and the scale small, and loses bits
+      // where x is tiny.  (fmaf with 0, for a scale in fp16 is an operand of it.)
 #pragma unroll
-      for (int v = 0; v < 4; v++) acc[v] = fmaf(q.sc.get(g, v), d[v] * f, acc[v]);
+      for (int v = 0; v < 4; v++) acc[v] = fmaf(fmaf(q.sc.get(g, v), d[v], 0.0f), f, acc[v]);
     }
   };
   auto multiplied = [&]() {  // a whole unit

@@ -1,0 +1,59 @@
+"""GPU: 4-bit linears whose activations and scales lie far apart, so that their
+product is an ordinary number and a step on the way to it need not be.
+
+Tolerance: that of the other parity tests of these linears.  Their bound holds one
+sum for each group at 2^-23 of M, twice an fp32 rounding; what is rounded besides
+is s times a group's sum, by 2^-24 of that group's part of M."""
+import numpy as np
+import pytest
+import torch
+
+import binary_rank_gemv_packed_amd as nq
+from tests.test_gpu_q4 import DEV, DT, check, make, pack
+
+pytestmark = pytest.mark.gpu
+
+# shared and split decode, both prompt tiles, K splits
+SHAPES = [(70, 300, 1), (70, 300, 16), (130, 9000, 7), (64, 28672, 16), (70, 300, 17), (40, 1100, 64), (70, 300, 65),
+          (130, 2179, 130)]
+
+
+def far(m, n, B, G, scale, xd, s_power, x_power):
+    q, s, z, x = make(m, n, B, G, True, scale, xd)
+    s = (s.double() * 2.0 ** s_power).to(DT[scale])
+    return q, s, z, (x.double() * 2.0 ** x_power).to(DT[xd])
+
+
+@pytest.mark.parametrize("m,n,B", SHAPES)
+@pytest.mark.parametrize("G", [32, 128])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,s_power", [("f16", -10), ("f32", -20), ("f32", -60)])
+@pytest.mark.parametrize("x_power", [113, 120])
+def test_large_activations_and_small_scales(m, n, B, G, xd, scale, s_power, x_power):
+    """Outputs of about 2^120 at most; a group's sum without its scale passes fp32."""
+    q, s, z, x = far(m, n, B, G, scale, xd, s_power, x_power)
+    check(nq.q4_linear(x.to(DEV), pack(q, s, z, G), out_dtype=torch.float32), x, q, s, z, G)
+
+
+@pytest.mark.parametrize("m,n,B", SHAPES)
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", ["f16", "f32"])
+def test_zero_scales_and_large_activations(m, n, B, xd, scale):
+    """A group whose scale is zero adds nothing, whatever its sum."""
+    q, s, z, x = far(m, n, B, 64, scale, xd, 0, 0)
+    block = slice(128, 256)  # whole, for columns beside them would share their power of two
+    x[:, block] = (x[:, block].double() * 2.0 ** 123).to(DT[xd])
+    s[:, 2:4] = 0
+    y = nq.q4_linear(x.to(DEV), pack(q, s, z, 64), out_dtype=torch.float32)
+    assert bool(torch.isfinite(y).all())
+    if B <= 16:  # above, the power of two is the row's
+        x[:, block] = 0
+        check(y, x, q, s, z, 64)
+
+
+@pytest.mark.parametrize("m,n,B", SHAPES)
+@pytest.mark.parametrize("G", [32, 128])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+def test_small_activations_and_large_scales(m, n, B, G, xd):
+    q, s, z, x = far(m, n, B, G, "f32", xd, 75, -90)
+    check(nq.q4_linear(x.to(DEV), pack(q, s, z, G), out_dtype=torch.float32), x, q, s, z, G)
