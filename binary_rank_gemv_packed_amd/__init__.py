@@ -452,8 +452,9 @@ def q4_pack(codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | Non
             stream=None) -> Q4Layer:
     """Packs the 4-bit weight W[i, j] = scales[i, j // group] * (codes[i, j] -
     zeros[i, j // group]) already on the GPU: codes uint8 (m, n) in 0..15, scales
-    fp16 or fp32 (m, ceil(n / group)), zeros uint8 of that shape in 0..15 or None
-    for 8 everywhere; group 32, 64 or 128.  Blocks until validation is done."""
+    fp16 or fp32 (m, ceil(n / group)) and below 2^80 where finite, zeros uint8 of that
+    shape in 0..15 or None for 8 everywhere; group 32, 64 or 128.  Blocks until
+    validation is done."""
     if codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_cuda:
         raise NQError(NQ_ERR_INVALID_ARG, "codes must be a uint8 GPU matrix")
     if scales.dtype not in (torch.float16, torch.float32):

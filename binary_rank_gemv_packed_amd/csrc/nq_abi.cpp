@@ -771,7 +771,8 @@ nq_status nq_q4_pack(const nq_q4_layer* L, const uint8_t* codes, const void* sca
   e = hipMemcpyAsync(&bad_host, bad, sizeof(int), hipMemcpyDeviceToHost, s);
   if (e == hipSuccess) e = hipStreamSynchronize(s);
   if (e != hipSuccess) return hip_fail(e, "4-bit pack synchronise");
-  if (bad_host) return fail(NQ_ERR_RANGE, "a code or zero point is above 15");
+  if (bad_host & nq::Q4_BAD_CODE) return fail(NQ_ERR_RANGE, "a code or zero point is above 15");
+  if (bad_host) return fail(NQ_ERR_RANGE, "a scale has a finite magnitude of 2^80 or more");
   return ok();
 }
 
@@ -1079,7 +1080,7 @@ const char* nq_status_string(int32_t s) {
     case NQ_ERR_UNSUPPORTED: return "unsupported by the chosen path";
     case NQ_ERR_HIP: return "HIP runtime error";
     case NQ_ERR_INTERNAL: return "internal error";
-    case NQ_ERR_RANGE: return "4-bit code or zero point above 15";
+    case NQ_ERR_RANGE: return "4-bit code or zero point above 15, or scale of 2^80 or more";
   }
   return "unknown status";
 }

@@ -175,11 +175,16 @@ __host__ __device__ inline float plane_factor(int k) {
 // ---------------------------------------------------------------------------
 constexpr uint32_t Q4_MAGIC = 0x3134514eu;  // "NQ41"
 constexpr uint32_t Q4_VERSION = 1;
+constexpr int Q4_BAD_CODE = 1;   // a code or zero point above 15
+constexpr int Q4_BAD_SCALE = 2;  // a finite scale of Q4_SCALE_LIMIT or more
+// A row's sum of scale x (code - zero) x (x as fp16, below 2^15) over 2^20 columns
+// stays below 2^80+4+15+20 = 2^119, whatever power of two x still lacks.
+constexpr float Q4_SCALE_LIMIT = 0x1p80f;
 
 struct Q4Header {
   uint32_t magic, version;
   int32_t m, n, group, scale_dtype, zeros;
-  int32_t bad;  // set by the pack kernels when a code or zero point is above 15
+  int32_t bad;  // Q4_BAD_* that the pack kernels met
   uint64_t off_codes, off_scales, off_zeros, total;
 };
 

@@ -15,7 +15,8 @@
 // rounded value and its rounded remainder, off by at most 2^-22 of itself.  So
 // the products are exact or nearly so, the sums over a group are held by the
 // fp16 MFMA in fp32; s multiplies the group's sum and then the block's power of two
-// the product, both in fp32.  y is rounded once.
+// the product, both in fp32 (in the prompt kernel once for the whole row, whose
+// sum of s times integers stays below 2^119 by Q4_SCALE_LIMIT).  y is rounded once.
 #include "nq_common.h"
 #include "nq_internal.h"
 
@@ -65,22 +66,27 @@ __global__ void __launch_bounds__(256) q4_pack_codes_kernel(const uint8_t* __res
         word |= (c & 15u) << (4 * p);
       }
     out[id] = word;
-    if (bad) atomicOr(bad_flag, 1);
+    if (bad) atomicOr(bad_flag, Q4_BAD_CODE);
   }
 }
 
 // One thread per entry of the scales (quad = 4: four rows of a group together)
-// or the zero points (quad = 1: a row's groups together).
+// or the zero points (quad = 1: a row's groups together).  Zero points above 15
+// and fp32 scales of a finite magnitude of Q4_SCALE_LIMIT or more are reported.
 template <typename T>
 __global__ void __launch_bounds__(256) q4_pack_groups_kernel(const T* __restrict__ in, int m, int ng, int KT, int SG,
                                                              int quad, long long entries, T* __restrict__ out,
-                                                             int limit, int* __restrict__ bad_flag) {
+                                                             int* __restrict__ bad_flag) {
   for (long long id = (long long)blockIdx.x * 256 + threadIdx.x; id < entries; id += (long long)gridDim.x * 256) {
     int row, g;
     q4_group_entry(id, KT, SG, quad, &row, &g);
     T v = 0;
     if (row < m && g < ng) v = in[(size_t)row * ng + g];
-    if (limit && (int)v > limit) atomicOr(bad_flag, 1);
+    if (sizeof(T) == 1 && v > 15) atomicOr(bad_flag, Q4_BAD_CODE);
+    if (sizeof(T) == 4) {
+      const float scale = fabsf(__uint_as_float((uint32_t)v));
+      if (scale >= Q4_SCALE_LIMIT && scale < INFINITY) atomicOr(bad_flag, Q4_BAD_SCALE);
+    }
     out[id] = v;
   }
 }
@@ -1034,13 +1040,13 @@ hipError_t q4_pack(const Q4Layout& lay, int m, int n, int group, int scale_bytes
                      reinterpret_cast<uint32_t*>(blob + lay.off_codes), bad);
   if (scale_bytes == 2)
     hipLaunchKernelGGL((q4_pack_groups_kernel<uint16_t>), ge, dim3(256), 0, st, static_cast<const uint16_t*>(s), m, ng,
-                       KT, SG, 4, entries, reinterpret_cast<uint16_t*>(blob + lay.off_scales), 0, bad);
+                       KT, SG, 4, entries, reinterpret_cast<uint16_t*>(blob + lay.off_scales), bad);
   else
     hipLaunchKernelGGL((q4_pack_groups_kernel<uint32_t>), ge, dim3(256), 0, st, static_cast<const uint32_t*>(s), m, ng,
-                       KT, SG, 4, entries, reinterpret_cast<uint32_t*>(blob + lay.off_scales), 0, bad);
+                       KT, SG, 4, entries, reinterpret_cast<uint32_t*>(blob + lay.off_scales), bad);
   if (z)
     hipLaunchKernelGGL((q4_pack_groups_kernel<uint8_t>), ge, dim3(256), 0, st, z, m, ng, KT, SG, 1, entries,
-                       blob + lay.off_zeros, 15, bad);
+                       blob + lay.off_zeros, bad);
   return hipGetLastError();
 }
 

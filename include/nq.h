@@ -47,7 +47,7 @@ typedef enum {
   NQ_ERR_UNSUPPORTED = -4, /* valid arguments that the chosen path does not handle                */
   NQ_ERR_HIP = -5,         /* a HIP runtime call or launch failed; see nq_last_error()           */
   NQ_ERR_INTERNAL = -6,
-  NQ_ERR_RANGE = -7        /* a 4-bit code or zero point is above 15 (nq_q4_pack only)            */
+  NQ_ERR_RANGE = -7        /* a 4-bit code, zero point or scale out of range (nq_q4_pack only)    */
 } nq_status;
 
 typedef enum { NQ_F32 = 0, NQ_F16 = 1, NQ_BF16 = 2 } nq_dtype;
@@ -281,10 +281,12 @@ size_t nq_q4_layer_bytes(int32_t m, int32_t n, int32_t group, int32_t scale_dtyp
 
 /* Packs codes, scales and zero points into L->blob.
  *   codes  : device, m x n uint8 row-major, every code in 0..15
- *   scales : device, m x ceil(n / group) row-major (L->scale_dtype)
+ *   scales : device, m x ceil(n / group) row-major (L->scale_dtype), each below 2^80
+ *            in magnitude if it is finite
  *   zeros  : device, m x ceil(n / group) uint8 row-major in 0..15 if L->zeros, else NULL
- * NQ_ERR_RANGE when a code or zero point is above 15 (the blob is then
- * unusable).  BLOCKING on `stream`; the inputs may be freed afterwards. */
+ * NQ_ERR_RANGE when a code or zero point is above 15 or a scale is out of range
+ * (the blob is then unusable).  An infinite or NaN scale is kept and makes its row's
+ * outputs infinities or NaN.  BLOCKING on `stream`; the inputs may be freed afterwards. */
 nq_status nq_q4_pack(const nq_q4_layer* L, const uint8_t* codes, const void* scales, const uint8_t* zeros,
                      nq_stream_t stream);
 

@@ -57,3 +57,39 @@ def test_zero_scales_and_large_activations(m, n, B, xd, scale):
 def test_small_activations_and_large_scales(m, n, B, G, xd):
     q, s, z, x = far(m, n, B, G, "f32", xd, 75, -90)
     check(nq.q4_linear(x.to(DEV), pack(q, s, z, G), out_dtype=torch.float32), x, q, s, z, G)
+
+
+# ------------------------------------------------------------------ scales at pack time
+@pytest.mark.parametrize("B", [1, 17, 130])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_the_largest_scale_that_is_taken(B, sign):
+    """Every scale just below 2^80, and activations that make the outputs ordinary: no
+    sum on the way passes fp32 in either kernel."""
+    q, s, z, x = far(40, 300, B, 32, "f32", "f32", 0, -90)
+    s = torch.full_like(s, sign * 2.0 ** 80 * (1 - 2.0 ** -24))
+    check(nq.q4_linear(x.to(DEV), pack(q, s, z, 32), out_dtype=torch.float32), x, q, s, z, 32)
+
+
+@pytest.mark.parametrize("value", [2.0 ** 80, -2.0 ** 80, 2.0 ** 110, -3.4e38])
+@pytest.mark.parametrize("zeros", [True, False])
+def test_larger_scales_are_refused(value, zeros):
+    """From 2^102 on, a prompt's sum of scale times integers passes fp32 before the
+    power of two of a small x is applied, where the same call for 16 rows was right."""
+    q, s, z, _ = make(40, 300, 1, 64, zeros, "f32", "f32")
+    s[39, 4] = value
+    with pytest.raises(nq.NQError) as e:
+        pack(q, s, z, 64)
+    assert e.value.status == nq.NQ_ERR_RANGE and "scale" in str(e.value)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("scale", ["f16", "f32"])
+@pytest.mark.parametrize("B", [2, 30])
+def test_infinite_and_nan_scales_stay_in_their_row(value, scale, B):
+    q, s, z, x = make(40, 300, B, 64, True, scale, "bf16")
+    ref = nq.q4_linear(x.to(DEV), pack(q, s, z, 64), out_dtype=torch.float32)
+    s[21, 4] = value
+    y = nq.q4_linear(x.to(DEV), pack(q, s, z, 64), out_dtype=torch.float32)
+    assert not torch.isfinite(y[:, 21]).any()
+    keep = [i for i in range(40) if i != 21]
+    assert torch.equal(y[:, keep], ref[:, keep])
