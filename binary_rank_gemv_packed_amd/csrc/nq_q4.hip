@@ -11,7 +11,7 @@
 // has put the largest magnitude of its block (128 columns of a row in the
 // decode kernel, the row in the prompt kernel) into [2^14, 2^15): a bf16 value
 // keeps its eight bits down to 2^-32 of the block's largest, and what is lost
-// below is under 2^-39 of it.  An fp32 value is taken as two fp16 pieces, the
+// below is under 2^-39 of it, or under 2^-144.  An fp32 value is taken as two fp16 pieces, the
 // rounded value and its rounded remainder, off by at most 2^-22 of itself.  So
 // the products are exact or nearly so, the sums over a group are held by the
 // fp16 MFMA in fp32; s multiplies the group's sum and then the block's power of two
@@ -258,7 +258,7 @@ struct Q4X<uint16_t> {
 
 // Power of two that puts a block whose largest magnitude has these bits (of an
 // fp32 number, below infinity) into fp16: the largest times 2^e lies in
-// [2^14, 2^15).  e <= 120 keeps 2^-e a normal number.
+// [2^14, 2^15).  e <= 120 keeps 2^-e a normal number; fp16 then ends at 2^-24-120.
 __device__ __forceinline__ int q4_block_exp(uint32_t mx) {
   const int e = 14 + 127 - (int)(mx >> 23);
   return mx == 0 ? 0 : e < 120 ? e : 120;

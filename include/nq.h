@@ -306,7 +306,8 @@ size_t nq_q4_workspace_bytes(const nq_q4_layer* L, int32_t B);
  *       NULL when that is 0
  * The products are exact or off by at most 2^-22, sums are fp32, y is rounded
  * once.  (Within a row of x, for B up to 16 within 128 columns of it, parts
- * under 2^-39 of the largest finite value are dropped.)  An infinity or NaN in
+ * under 2^-39 of the largest finite value are dropped, and so are parts under
+ * 2^-144 of an fp32 x.)  An infinity or NaN in
  * a row of x makes every output of that row an infinity or NaN and leaves the
  * other rows alone.  ASYNCHRONOUS and re-entrant like nq_linear_fwd; may be
  * captured into a HIP graph; calls that overlap in time need workspaces of their

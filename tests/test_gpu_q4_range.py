@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import binary_rank_gemv_packed_amd as nq
-from tests.test_gpu_q4 import DEV, DT, check, make, pack
+from oracle import nq_q4 as Q
+from tests.test_gpu_q4 import DEV, DT, check, f64, make, pack
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,22 @@ def test_infinite_and_nan_scales_stay_in_their_row(value, scale, B):
     assert not torch.isfinite(y[:, 21]).any()
     keep = [i for i in range(40) if i != 21]
     assert torch.equal(y[:, keep], ref[:, keep])
+
+
+# ------------------------------------------------------------------ the smallest activations
+@pytest.mark.parametrize("B", [1, 16, 17, 130])
+@pytest.mark.parametrize("xd", ["bf16", "f32"])
+@pytest.mark.parametrize("x_power", [-115, -128, -138])
+def test_activations_below_the_normal_numbers(B, xd, x_power):
+    """Besides the usual bound, half a step of 2^-144 for each fp32 x; a bf16 x is a
+    multiple of 2^-133 and loses nothing."""
+    m, n, G = 70, 300, 64
+    q, s, z, x = far(m, n, B, G, "f32", xd, 75, x_power)
+    y = nq.q4_linear(x.to(DEV), pack(q, s, z, G), out_dtype=torch.float32)
+    ref, M = Q.linear(f64(x), q, f64(s), z, G), Q.magnitude(f64(x), q, f64(s), z, G)
+    chain = 128 * (2 if xd == "f32" else 1) + -(-n // G) + 32
+    tol = (chain * 2.0 ** -23 + 2.0 ** -22) * M
+    tol = tol + 2.0 ** -39 * np.abs(f64(x)).max(1, keepdims=True) * np.abs(Q.weight(q, f64(s), z, G)).sum(1)
+    if xd == "f32":
+        tol = tol + 2.0 ** -145 * np.abs(Q.weight(q, f64(s), z, G)).sum(1)
+    assert np.all(np.abs(f64(y) - ref) <= tol)
