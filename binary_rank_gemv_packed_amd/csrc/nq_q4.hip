@@ -19,6 +19,7 @@
 // sum of s times integers stays below 2^119 by Q4_SCALE_LIMIT).  y is rounded once.
 #include "nq_common.h"
 #include "nq_internal.h"
+#include "nq_q4_lds.h"
 
 #include <type_traits>
 
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(1024) q4_dec_kernel(Q4DecArgs a) {
   const int k_lo = split * a.range, k_hi = min(KT, k_lo + a.range), KR = a.range;
   _Float16* img = reinterpret_cast<_Float16*>(smem);                        // [P][KR][B][128]
   float* xfac = reinterpret_cast<float*>(smem + (size_t)P * KR * B * 256);  // [KR][B]
-  float* red = xfac + KR * B;                                               // [keep][W][B][16]
+  float* red = xfac + q4_dec_fac_floats(B, KR);                             // [keep][W][B][16]
 
   const bool shared = a.shared;
   const int wr = shared ? 0 : wave, WR = shared ? 1 : W;
@@ -876,13 +877,13 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
   p.range = ceil_div(KT, p.S);
   p.S = ceil_div(KT, p.range);
   p.tpw = p.shared ? ceil_div(p.range, p.W) : p.range;
-  p.lds = per_tile * p.range;
   if (p.shared) {
-    const int turns = ceil_div(RT, p.groups), each = p.W * 16 * B * 4;
-    const int fit = (int)(((small ? MAX_LDS / 2 : MAX_LDS) - p.lds) / each);  // at least 2
+    const size_t most = small ? MAX_LDS / 2 : MAX_LDS, row_tile = q4_dec_lds(P, B, 0, p.W, 1).total;
+    const int turns = ceil_div(RT, p.groups);
+    const int fit = (int)((most - q4_dec_lds(P, B, p.range, p.W, 0).total) / row_tile);  // at least 2
     p.keep = turns < fit ? turns : fit;
-    p.lds += (size_t)p.keep * each;
   }
+  p.lds = q4_dec_lds(P, B, p.range, p.W, p.keep).total;
   p.part = p.S > 1 ? p.S * out * 4 : 0;
   return p;
 }
