@@ -153,6 +153,11 @@ def _gpu_tensor(t: torch.Tensor, name: str, dtype, shape, device) -> None:
                                           f"{device} (got {t.dtype} {tuple(t.shape)} on {t.device})")
 
 
+def _scratch(workspace: torch.Tensor, device) -> None:
+    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise NQError(NQ_ERR_INVALID_ARG, f"the workspace must be a contiguous uint8 tensor on {device}")
+
+
 class Layer:
     """A packed layer: the device blob plus its dimensions."""
 
@@ -519,11 +524,6 @@ def _q4_output(x: torch.Tensor, B: int, y: torch.Tensor, m: int, dtype: torch.dt
     _gpu_tensor(y, "y", dtype, (B, m) if x.dim() == 2 else (m,), x.device)
 
 
-def _q4_scratch(workspace: torch.Tensor, device) -> None:
-    if workspace.dtype != torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-        raise NQError(NQ_ERR_INVALID_ARG, f"the workspace must be a contiguous uint8 tensor on {device}")
-
-
 def q4_linear_into(x: torch.Tensor, layer: Q4Layer, y: torch.Tensor, workspace: torch.Tensor,
                    stream=None) -> torch.Tensor:
     """y = x W^T into caller buffers, x (B, n) or (n,) bf16 or fp32, y (B, m) or
@@ -532,7 +532,7 @@ def q4_linear_into(x: torch.Tensor, layer: Q4Layer, y: torch.Tensor, workspace: 
     device = layer.device
     B = _q4_batch(x, layer.n, device)
     _q4_output(x, B, y, layer.m, y.dtype)
-    _q4_scratch(workspace, device)
+    _scratch(workspace, device)
     _on_stream(device, stream, lambda s: _check(lib().nq_q4_linear_fwd(
         layer.ref, x.data_ptr(), _DT[x.dtype], y.data_ptr(), _DT[y.dtype], B, workspace.data_ptr(),
         workspace.numel(), s)))
@@ -562,7 +562,7 @@ def q4_linear_group_into(x: torch.Tensor, layers, ys, workspace: torch.Tensor, s
         raise NQError(NQ_ERR_INVALID_ARG, "one output per layer")
     for y, L in zip(ys, group.layers):
         _q4_output(x, B, y, L.m, ys[0].dtype)
-    _q4_scratch(workspace, group.device)
+    _scratch(workspace, group.device)
     yp = (ctypes.c_void_p * len(ys))(*[y.data_ptr() for y in ys])
     _on_stream(group.device, stream, lambda s: _check(lib().nq_q4_linear_fwd_group(
         group.ref, len(group), x.data_ptr(), _DT[x.dtype], yp, _DT[ys[0].dtype], B, workspace.data_ptr(),
@@ -669,6 +669,8 @@ def block_norm_backward(dx: torch.Tensor | None, dh: torch.Tensor | None, h: tor
     dxp = check(dx, "dx", norm.act_dtype, shape, dev)
     dhp, gp = check(dh, "dh", norm.res_dtype, shape, dev), check(gate, "gate", norm.act_dtype, shape, dev)
     sp = check(stats, "stats", f32, (2, rows), dev)
+    if workspace is not None:
+        _scratch(workspace, dev)
     if inplace and dh is None:
         raise NQError(NQ_ERR_INVALID_ARG, "inplace needs dh")
 
