@@ -786,6 +786,8 @@ nq_status nq_q4_unpack(const nq_q4_layer* L, uint8_t* codes, uint8_t* zeros, nq_
   if (spans_overlap(L->blob, lay.total, codes, (size_t)L->m * L->n) ||
       (zeros && spans_overlap(L->blob, lay.total, zeros, groups)))
     return fail(NQ_ERR_INVALID_ARG, "the blob and an output overlap");
+  if (zeros && spans_overlap(codes, (size_t)L->m * L->n, zeros, groups))
+    return fail(NQ_ERR_INVALID_ARG, "codes and zeros overlap");
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   (void)hipGetLastError();
   hipError_t e = nq::q4_unpack(lay, L->m, L->n, L->group, static_cast<const uint8_t*>(L->blob), codes, zeros, s);

@@ -42,3 +42,13 @@ def test_norm_backward_refuses_a_workspace_of_another_kind(ws):
     t = [Stand((ROWS, D), f32) for _ in range(4)]
     with pytest.raises(nq.NQError, match="workspace"):
         nq.block_norm_backward(t[0], t[1], t[2], t[3], Stand((2, ROWS), f32), norm, workspace=ws)
+
+
+def test_unpack_refuses_outputs_on_each_other():
+    """Codes (64 x 96 bytes) and zero points (64 x 3 bytes) written into one another."""
+    import ctypes
+    fake, far = 0x7F0000000000, 0x7F0040000000
+    lay = nq.nq_q4_layer(64, 96, 32, nq.NQ_F16, 1, fake)
+    for zeros in (far, far + 64 * 96 - 1, far - 64 * 3 + 1):
+        assert nq.lib().nq_q4_unpack(ctypes.byref(lay), far, zeros, None) == nq.NQ_ERR_INVALID_ARG
+        assert b"overlap" in nq.lib().nq_last_error()
