@@ -12,8 +12,10 @@
 //   s  = v gate (w_post + o),  dy = ry (s - yn mean(s yn)),  dw_post = sum of v gate yn over rows
 //
 // All arithmetic is fp32; each output is rounded once, to its type (x is formed
-// from h' before its rounding).  The row stays in registers from its one read
-// to its one write.
+// from h' before its rounding).  The row stays in registers from its one read to
+// its one write: forward up to 16384 columns, backward up to 4096, and up to 8192 but
+// for a few registers of some types.  Wider rows pass through scratch memory in part,
+// see the kernels.
 #include "nq_common.h"
 #include "nq_internal.h"
 
@@ -159,8 +161,10 @@ __device__ __forceinline__ float norm_rstd(float ss, int d, float eps) { return 
 // ------------------------------------------------------------------ forward
 // While the registers hold it, everything is asked for before the first sum: with
 // few rows the kernel's time is that of one read.  One row of 8192: 4.85 us (5.4 us
-// with each read where it is used); 2048 rows with an fp32 stream: 42.2 us,
-// 4.8 TB/s, where a 1 GiB copy moves 5.2.
+// with each read where it is used); 2048 rows with an fp32 stream: 42.2 us a call
+// among others, 4.8 TB/s (38.6 us by itself in a kernel trace), where a 1 GiB copy
+// moves 5.2; 1024 x 16384 50 us, 4.0 TB/s.  Four chunks a thread (above 16384 columns)
+// spill 28 to 436 bytes a lane in 9 of their 18 variants: 512 x 28672 46 us, 3.8 TB/s.
 template <typename HT, typename AT, typename PT, bool WHOLE, int C>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(NormArgs a) {
   constexpr bool EARLY = C == 1 || (C == 2 && sizeof(AT) == 2);
@@ -250,8 +254,15 @@ struct NormBwdRow {
 // memory (w_pre, w_post, gate, each [thread][8]), for a read of them from memory
 // would have to wait for the next row's, which is ahead of it.
 // Up to 512 threads (4096 columns) a thread may have 256 registers, and none of
-// this leaves them.  4096 x 8192 with an fp32 stream: 118 us, 5.1 TB/s (149 us
-// with 512 workgroups, no row ahead and the weights read from memory).
+// this leaves them.  4096 x 8192 with an fp32 stream: 123 us with the join, 4.9 TB/s
+// (149 us with 512 workgroups, no row ahead and the weights read from memory).
+// 1024 threads have 128 registers each.  One chunk a thread then spills 12 bytes a lane
+// with an fp32 stream and weights, 48 to 52 with an fp32 branch, and 68 to 160 where
+// rows are not whole 16-byte pieces (1024 x 6001, 52 us, 2.1 TB/s).  Two and four
+// chunks, whose two sums over rows alone are 32 and 64 registers beside the row and its
+// gradients, spill 348 to 1960 bytes inside the row loop: 1024 x 16384 with an fp32
+// stream 235 us, four times its bytes' time, and 1209 us with all of it bf16, where
+// elementary operations take 791 us.
 template <typename HT, typename AT, typename PT, bool WHOLE, int C, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_bwd_kernel(NormArgs a) {
   constexpr bool AHEAD = C == 1;

@@ -336,7 +336,8 @@ struct Q4Tile {
 // result has row 4 (lane >> 4) + v of the tile for b = lane & 15.  Lanes with
 // b >= B repeat row B - 1 and are not stored.
 // Bound by the reads: gate and up of a 70B block (2 x 28672 x 8192, one row) take
-// 46.5 us, 5.25 TB/s, a bare read of as many bytes 37.9 us; one 8192 x 8192 9.7 us.
+// 45 to 47 us over runs, 5.2 TB/s, a bare read of as many bytes 37.9 us; one 8192 x
+// 8192 9.7 to 10.2 us.
 // A tile costs a wave about 70 vector instructions, half the issue slots.
 // STREAM: codes that no cache will hold until the next call are read past the
 // caches' replacement (host side: q4_streams).
@@ -642,8 +643,13 @@ __device__ __forceinline__ void wait_vmem() { asm volatile("s_waitcnt vmcnt(0)" 
 // 215 us against 200 us; 34 x 9728 -> 8832 with groups of 32, 78 against 41 us.)
 // A K step is one column tile (128 columns): its x goes from memory straight to
 // shared memory one step ahead, the codes of the wave's two row tiles to registers
-// one step ahead.  2048 x 4096 -> 11008: 198 us with q4_rows_kernel, 933 TFLOP/s;
-// matrix unit busy 0.39 of the time, vector issue 0.38.
+// one step ahead.  2048 x 4096 -> 11008, groups of 128: 199 to 205 us with
+// q4_rows_kernel over runs, 900 to 930 TFLOP/s (each launch by itself in a kernel
+// trace: 217 and 8.5 us); matrix unit busy 0.39 of the time, vector issue 0.38.
+// The launch bound fits groups of 128.  Groups of 64 with fp16 scales need about
+// 340 registers and have 256: 192 to 216 bytes a lane go through scratch memory in
+// the K loop, 849 us for the same product (groups of 32, 483 us; fp32 x, one wave a
+// SIMD, 498 us).
 template <typename ST, int SG, bool ZERO, int P, int NC>
 __global__ void __launch_bounds__(256, NC == 4 || (P == 1 && SG * sizeof(ST) <= 4) ? 2 : 1)
     q4_gemm_kernel(Q4GemmArgs a) {
@@ -849,16 +855,22 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
   }
   const size_t per_tile = (size_t)B * (256 * P + 4);  // of the image of x
   const bool small = per_tile * KT <= 40 * 1024;
-  // a large image for few row tiles is not worth turning over whole: 1100 x 4099,
-  // 7 rows of fp32 (116 KB, 69 row tiles), 13.7 us shared, 12.0 us split
+  // An image of 64 to 128 KB is turned over whole by every workgroup, or split.  us
+  // shared / split, for 7 rows of 4099 fp32, 7 of 8192 and 5 of 11008 bf16:
+  //   69 row tiles  11.6 / 10.8  10.7 / 10.9  12.9 / 11.6
+  //   127           11.6 / 10.9  10.7 / 11.0  13.1 / 12.9
+  //   129           11.6 / 10.9  10.7 / 11.5  13.1 / 13.1
+  //   256           11.7 / 13.6  11.8 / 12.6  13.7 / 13.2
+  //   512           14.5 / 13.9  14.1 / 14.7  18.5 / 18.9
+  // so few row tiles are split and many share; no size of the three is best all along.
   p.shared = per_tile * KT <= (RT < 128 ? 64 : 128) * 1024;
   if (p.shared) {
     // the whole row of x fits: the waves of a workgroup share each row tile, four
     // column tiles a wave where there are as many.  A small image (one row of x, two
     // of 8192) is turned over twice rather than once, and two workgroups of 8 waves
-    // a CU do not wait for each other: 8192 x 8192, 10.9 -> 10.2 us, gate and up of a
-    // 70B block 48 -> 46 us; with four rows
-    // of 8192 the turning over costs more, 31.5 -> 34.3 us for 32000 rows of W.
+    // a CU do not wait for each other: 8192 x 8192, 11.2 -> 10.2 us, 57344 x 8192
+    // 45.3 -> 44 us, two rows 11.5 -> 11.3 us.  Four rows of 8192 gain nothing: 8192
+    // rows of W 11.8 us against 12.0 us with two workgroups, 32000 29.7 us either way.
     const int most = small ? 8 : 16, w = ceil_div(KT, 4);
     p.W = w < most ? w : most;
     p.S = 1;
@@ -888,9 +900,11 @@ Q4DecPlan q4_dec_plan(const int* m, int L, int n, int B, int P) {
   return p;
 }
 
-// Codes of 16 MB or more are read as a stream: 8192 x 8192, 10.5 -> 10.2 us, gate and
-// up of a 70B block 48.3 -> 46 us; below, what the caches keep is worth more:
-// 4096 x 4096 (8 MB), 5.5 us against 5.9 us read as a stream.
+// Codes of 16 MB or more are read as a stream.  One row, us as a stream / not, over
+// 1 GiB of weights in turn: 32000 x 8192 (131 MB) 27.6 / 28.4, 8192 x 8192 (34 MB)
+// 10.2 / 10.5, 11008 x 4096 (23 MB) 8.55 / 8.42, 4096 x 8192 (17 MB) 7.1 / 7.3, 4096 x
+// 4096 (8 MB) 5.9 / 5.8, 2048 x 4096 5.4 / 5.3; with weights that stay in the 256 MB
+// cache 4096 x 4096 5.6 / 5.5 and 2048 x 4096 5.3 / 4.9.
 bool q4_streams(const Q4DecArgs& k) { return (size_t)k.rows * k.KT * 1024 >= (size_t)16 << 20; }
 
 template <typename XT>
@@ -927,7 +941,9 @@ hipError_t dec_forward(const Q4Args& a) {
     using ST = decltype(st);
     constexpr int SG = decltype(sg)::value, bytes = SG * sizeof(ST);
     // tiles in flight (U D): as many as the registers of 16 waves a CU hold beside
-    // the operands
+    // the operands of a bf16 x (groups of 32 with fp32 scales and zero points: 12
+    // bytes a lane spill).  fp32 x has twice the operands, and 14 of its 24 variants
+    // spill 8 to 80 bytes a lane.
     constexpr int U = bytes == 2 ? 4 : bytes <= 8 ? 2 : 1, D = bytes == 4 || bytes == 16 ? 3 : 2;
     k.steps = ceil_div(p.tpw, U);
     constexpr bool Z = decltype(zero)::value;
@@ -955,7 +971,9 @@ Q4GemmPlan q4_gemm_plan(int m, int n, int B, int x_dtype) {
   p.NC = B <= 64 ? 4 : 8;
   const long long tiles = (long long)ceil_div(m, QM) * ceil_div(B, 16 * p.NC);
   // K splits while the tiles leave CUs idle, each of at least four steps: 8192 x 8192,
-  // 20 rows 64 -> 22 us, 128 rows 92 -> 38 us; 4096 x 4096, 512 rows 180 -> 90 us
+  // 20 rows 64 -> 22 us, 128 rows 92 -> 38 us.  (The floor of such a batch, one read
+  // of the codes, is 5 to 7 us: three launches, a K step's latency and the partial
+  // sums' way through memory are in the rest.)
   int S = 1;
   while (tiles * S < 384 && S < 32 && KT / (2 * S) >= 4) S *= 2;
   p.S = ceil_div(KT, ceil_div(KT, S));
