@@ -1,6 +1,8 @@
 """Python binding of libnq: linear layers with a low-rank binary-factorised weight
 W_hat = diag(s1) U diag(g) V^T diag(s2) on MI355X, and what stands beside them in a
-model: linears with 4-bit weights (q4_*) and the norms between blocks (block_norm).
+model: linears with 4-bit weights (q4_*), the norms between blocks (block_norm), the
+norms and rotation of heads (head_norm), a paged cache of keys and values (kv_write,
+kv_read) and one token's attention over it (kv_attention).
 
 Argument marshalling only: every step of the forward runs in the HIP kernels of
 libnq.so, reached through its C ABI (include/nq.h).  PyTorch provides device
@@ -23,6 +25,8 @@ NQ_F32, NQ_F16, NQ_BF16 = 0, 1, 2
 NQ_GROUP_MAX = 4  # layers per group call (include/nq.h)
 NQ_ENVELOPE_MAX = 4  # terms of a rank-l envelope (include/nq.h)
 NQ_NORM_POST, NQ_NORM_PRE, NQ_NORM_MAX_DIM = 1, 2, 32768  # block norms (include/nq.h)
+NQ_HEAD_NORM, NQ_HEAD_INTERLEAVED, NQ_HEAD_MAX_AXES = 1, 2, 4  # head norms (include/nq.h)
+KV_KINDS = {"bf16": 0, "int8": 1, "int4": 2}  # how a cache holds its values (include/nq.h)
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "valu": 3, "decode": 4}
 
 _DT = {torch.float32: NQ_F32, torch.float16: NQ_F16, torch.bfloat16: NQ_BF16}
@@ -52,6 +56,19 @@ class nq_block_norm(ctypes.Structure):
                 ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
 
 
+class nq_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("kind", ctypes.c_int32), ("data", ctypes.c_void_p)]
+
+
+class nq_head_norm(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("flags", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * NQ_HEAD_MAX_AXES), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -65,6 +82,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     c_int, c_size, vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
     P, Q, N = ctypes.POINTER(nq_layer), ctypes.POINTER(nq_q4_layer), ctypes.POINTER(nq_block_norm)
+    K, H, c_long = ctypes.POINTER(nq_kv_cache), ctypes.POINTER(nq_head_norm), ctypes.c_int64
     sigs = {
         "nq_abi_version": (c_int, []),
         "nq_layer_bytes": (c_size, [c_int, c_int, c_int, c_int]),
@@ -99,6 +117,17 @@ def lib() -> ctypes.CDLL:
         "nq_block_norm_fwd": (c_int, [N, c_int, vp, vp, vp, vp, vp, vp, vp]),
         "nq_block_norm_workspace_bytes": (c_size, [N, c_int]),
         "nq_block_norm_bwd": (c_int, [N, c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, c_size, vp]),
+        "nq_kv_page_bytes": (c_size, [c_int, c_int, c_int, c_int]),
+        "nq_kv_write": (c_int, [K, c_int, vp, c_long, vp, c_long, c_int, vp, vp]),
+        "nq_kv_read": (c_int, [K, c_int, vp, vp, vp, c_int, vp]),
+        "nq_kv_attention_workspace_bytes": (c_size, [K]),
+        "nq_kv_attention": (c_int, [K, c_int, vp, c_int, c_int, vp, c_int, vp, c_int, c_int, ctypes.c_float, vp, c_int,
+                                    vp, c_size, vp]),
+        "nq_head_norm_fwd": (c_int, [H, c_int, vp, c_long, c_int, vp, c_long, c_int, vp, vp, vp, vp]),
+        "nq_head_norm_kv_write": (c_int, [H, c_int, vp, c_long, c_int, vp, c_long, vp, c_long, vp, K, vp, vp, vp]),
+        "nq_head_norm_workspace_bytes": (c_size, [H, c_int]),
+        "nq_head_norm_bwd": (c_int, [H, c_int, vp, vp, vp, c_long, c_int, vp, c_long, c_int, vp, vp, vp, vp, vp, vp,
+                                     c_size, vp]),
         "nq_bits_per_weight": (ctypes.c_double, [c_int, c_int, c_int, c_int]),
         "nq_rank_for_bits": (c_int, [c_int, c_int, ctypes.c_double, c_int]),
         "nq_status_string": (ctypes.c_char_p, [c_int]),
@@ -693,6 +722,275 @@ def block_norm_backward(dx: torch.Tensor | None, dh: torch.Tensor | None, h: tor
         _check(lib().nq_block_norm_bwd(norm.ref, rows, dxp, dhp, hp, yp, gp, sp, ptr("dh"), ptr("dy"),
                                        ptr("dgate") if rows_gate else None, ptr("dw_post"), ptr("dw_pre"),
                                        None if rows_gate else ptr("dgate"), ws.data_ptr(), ws.numel(), s))
+        return out
+
+    return _on_stream(dev, stream, call)
+
+
+# ------------------------------------------------------------------ cache of keys and values
+class KvCache:
+    """Keys and values of many sequences in `pages` pages of `page` slots (a multiple
+    of 16), a slot holding one token's `heads` heads of `head_dim` (64, 96, 128, 192 or
+    256) channels, as bf16 ("bf16") or as whole numbers of 8 ("int8", one scale for each
+    token and head) or 4 bits ("int4", one for 32 channels of it): nq_kv_cache.  `data`
+    (pages, bytes of a page) is uint8 in the kernels' own order; `into` gives that memory."""
+
+    def __init__(self, pages: int, heads: int, head_dim: int, page: int = 64, kind: str = "bf16", device="cuda",
+                 into: torch.Tensor | None = None):
+        if kind not in KV_KINDS:
+            raise NQError(NQ_ERR_INVALID_ARG, f"kind must be one of {', '.join(KV_KINDS)}")
+        nbytes = int(lib().nq_kv_page_bytes(heads, head_dim, page, KV_KINDS[kind]))
+        if nbytes == 0 or not 1 <= pages <= 1 << 24:
+            raise NQError(NQ_ERR_INVALID_ARG, f"invalid cache pages={pages} heads={heads} head_dim={head_dim} page={page}")
+        if into is not None:
+            if into.dtype != torch.uint8 or into.shape != (pages, nbytes) or not into.is_cuda or not into.is_contiguous():
+                raise NQError(NQ_ERR_INVALID_ARG, f"into must be a contiguous uint8 GPU tensor of shape {(pages, nbytes)}")
+        self.data = into if into is not None else torch.empty((pages, nbytes), dtype=torch.uint8, device=device)
+        self.pages, self.heads, self.head_dim, self.page, self.kind = pages, heads, head_dim, page, kind
+        self.page_bytes, self.device = nbytes, self.data.device
+        self.c = nq_kv_cache(pages, heads, head_dim, page, KV_KINDS[kind], self.data.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+
+def _head_rows(t: torch.Tensor, name: str, dtype, heads, D: int, device) -> int:
+    """Elements between the rows of a (tokens, heads, D) tensor whose tokens are
+    contiguous: a tensor of its own or a part of a wider linear's output."""
+    shape = t.shape
+    if t.dtype == dtype and t.device == device and len(shape) == 3 and shape[2] == D and (heads is None or
+                                                                                         shape[1] == heads):
+        if t.is_contiguous():
+            return shape[1] * D
+        s = t.stride()
+        if s[2] == 1 and (s[1] == D or shape[1] == 1):
+            return s[0]
+    raise NQError(NQ_ERR_INVALID_ARG, f"{name} must be a {dtype} tensor (tokens, {'heads' if heads is None else heads}, "
+                                      f"{D}) on {device}, each token contiguous (got {t.dtype} {tuple(shape)} on {t.device})")
+
+
+def _kv_slots(slots: torch.Tensor, tokens: int, device) -> None:
+    if slots.dtype != torch.int64 or slots.shape != (tokens,) or slots.device != device or not slots.is_contiguous():
+        raise NQError(NQ_ERR_INVALID_ARG, f"slots must be a contiguous int64 tensor of shape ({tokens},) on {device}")
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, cache: KvCache, slots: torch.Tensor, stream=None) -> None:
+    """Writes tokens' keys and values (tokens, heads, head_dim; bf16 or fp32, rows may be
+    parts of wider ones) to their slots (int64; place s % page of page s // page; a slot
+    outside the cache, a negative one say, is left out)."""
+    if k.dtype not in _ACT:
+        raise NQError(NQ_ERR_INVALID_ARG, "k and v must be bf16 or fp32")
+    ks = _head_rows(k, "k", k.dtype, cache.heads, cache.head_dim, cache.device)
+    vs = _head_rows(v, "v", k.dtype, cache.heads, cache.head_dim, cache.device)
+    tokens = k.shape[0]
+    if v.shape[0] != tokens:
+        raise NQError(NQ_ERR_INVALID_ARG, f"{tokens} keys and {v.shape[0]} values")
+    _kv_slots(slots, tokens, cache.device)
+    _on_stream(cache.device, stream, lambda s: _check(lib().nq_kv_write(
+        cache.ref, tokens, k.data_ptr(), ks, v.data_ptr(), vs, _DT[k.dtype], slots.data_ptr(), s)))
+
+
+def kv_read(cache: KvCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16, stream=None):
+    """(k, v), (tokens, heads, head_dim) each: the values that the slots hold; zeros for
+    a slot outside the cache."""
+    if dtype not in _ACT:
+        raise NQError(NQ_ERR_INVALID_ARG, "dtype must be bf16 or fp32")
+    tokens = slots.shape[0] if slots.dim() == 1 else -1
+    _kv_slots(slots, tokens, cache.device)
+
+    def call(s):
+        shape = (tokens, cache.heads, cache.head_dim)
+        k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+        _check(lib().nq_kv_read(cache.ref, tokens, slots.data_ptr(), k.data_ptr(), v.data_ptr(), _DT[dtype], s))
+        return k, v
+
+    return _on_stream(cache.device, stream, call)
+
+
+def kv_attention_workspace_bytes(cache: KvCache) -> int:
+    """Workspace of kv_attention over this cache, for any batch."""
+    return int(lib().nq_kv_attention_workspace_bytes(cache.ref))
+
+
+def new_kv_workspace(B: int, q_heads: int, cache: KvCache) -> torch.Tensor:
+    """A workspace for kv_attention of B sequences and q_heads heads (its size depends on
+    the cache alone)."""
+    return torch.empty(kv_attention_workspace_bytes(cache), dtype=torch.uint8, device=cache.device)
+
+
+def kv_attention_into(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lengths: torch.Tensor, y: torch.Tensor,
+                      workspace: torch.Tensor, scale: float | None = None, window: int = 0, max_length: int = 0,
+                      stream=None) -> torch.Tensor:
+    """kv_attention into caller buffers (safe to capture in a graph: lengths and table are
+    read by the kernels)."""
+    dev = cache.device
+    B, q_heads = (q.shape[0], q.shape[1]) if q.dim() == 3 else (-1, -1)
+    if q.dtype not in _ACT or y.dtype not in _ACT:
+        raise NQError(NQ_ERR_INVALID_ARG, "q and y must be bf16 or fp32")
+    _gpu_tensor(q, "q", q.dtype, (B, q_heads, cache.head_dim), dev)
+    _gpu_tensor(y, "y", y.dtype, q.shape, dev)
+    _gpu_tensor(lengths, "lengths", torch.int32, (B,), dev)
+    if table.dim() != 2:
+        raise NQError(NQ_ERR_INVALID_ARG, "table must be (sequences, pages)")
+    _gpu_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
+    _scratch(workspace, dev)
+    scale = cache.head_dim ** -0.5 if scale is None else scale
+    _on_stream(dev, stream, lambda s: _check(lib().nq_kv_attention(
+        cache.ref, B, q.data_ptr(), _DT[q.dtype], q_heads, table.data_ptr(), table.shape[1], lengths.data_ptr(),
+        max_length, window, scale, y.data_ptr(), _DT[y.dtype], workspace.data_ptr(), workspace.numel(), s)))
+    return y
+
+
+def kv_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lengths: torch.Tensor,
+                 scale: float | None = None, window: int = 0, max_length: int = 0,
+                 out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Attention of one new token a sequence: q (B, q_heads, head_dim) bf16 or fp32, over
+    the last `window` (0: all) of lengths[b] tokens (int32; the new one, already written,
+    among them), whose token t lies in slot t % page of page table[b, t // page] (int32).
+    Query head h reads key head h // (q_heads // heads); scale is head_dim ** -0.5 unless
+    given.  Returns (B, q_heads, head_dim) of q's dtype unless given; zeros for a length
+    of 0, NaN for one above max_length (what the host knows of the lengths; 0: what the
+    table holds) or a page outside the cache."""
+    def call(_):
+        ws = workspace if workspace is not None else new_kv_workspace(q.shape[0], q.shape[1], cache)
+        return kv_attention_into(q, cache, table, lengths, torch.empty_like(q, dtype=out_dtype), ws, scale, window,
+                                 max_length)
+
+    return _on_stream(cache.device, stream, call)
+
+
+# ------------------------------------------------------------------ head norms
+class HeadNorm:
+    """Norm of each head of queries and keys with weights w_q and w_k ((head_dim,) GPU
+    tensors of one dtype, fp32, fp16 or bf16, or None for 1; norm=False: no norm), and
+    the rotation of its first 2 * len(inv_freq) channels by position * inv_freq (fp64, or
+    anything that converts to it; None: no rotation), pairs (i, i + rot / 2) or, interleaved,
+    (2i, 2i + 1).  sections: how many of the pairs go by each axis of the positions, in
+    order (None: one axis).  See nq_head_norm in include/nq.h."""
+
+    def __init__(self, head_dim: int, act_dtype: torch.dtype = torch.bfloat16, w_q: torch.Tensor | None = None,
+                 w_k: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+                 sections=None, norm: bool = True, weight_offset: float = 0.0, eps: float = 1e-6):
+        given = [t for t in (w_q, w_k) if t is not None]
+        self.head_dim, self.act_dtype, self.w_q, self.w_k, self.norm = head_dim, act_dtype, w_q, w_k, norm
+        dtype = given[0].dtype if given else torch.float32
+        self.device = given[0].device if given else inv_freq.device if inv_freq is not None else None
+        for t, name in ((w_q, "w_q"), (w_k, "w_k")):
+            if t is not None:
+                _gpu_tensor(t, name, dtype, (head_dim,), self.device)
+        if act_dtype not in _ACT or dtype not in _DT:
+            raise NQError(NQ_ERR_INVALID_ARG, "heads must be bf16 or fp32, weights fp32, fp16 or bf16")
+        if given and not norm:
+            raise NQError(NQ_ERR_INVALID_ARG, "a weight for a norm that is left out")
+        if self.device is not None and self.device.type != "cuda":
+            raise NQError(NQ_ERR_INVALID_ARG, "the weights and inv_freq must be GPU tensors")
+        if inv_freq is not None and (inv_freq.dim() != 1 or inv_freq.device != self.device):
+            raise NQError(NQ_ERR_INVALID_ARG, f"inv_freq must be one row on {self.device}")
+        self.inv_freq = inv_freq.double().contiguous() if inv_freq is not None else None
+        pairs = inv_freq.shape[0] if inv_freq is not None else 0
+        self.sections = tuple(int(n) for n in sections) if sections is not None else (pairs,)
+        self.axes = len(self.sections)
+        if not 1 <= self.axes <= NQ_HEAD_MAX_AXES or sum(self.sections) != pairs or min(self.sections) < 0:
+            raise NQError(NQ_ERR_INVALID_ARG, f"sections {self.sections} for {pairs} pairs and up to {NQ_HEAD_MAX_AXES} axes")
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self.c = nq_head_norm(head_dim, NQ_HEAD_NORM * bool(norm) | NQ_HEAD_INTERLEAVED * bool(interleaved),
+                              _DT[act_dtype], _DT[dtype], 2 * pairs, self.axes,
+                              (ctypes.c_int32 * NQ_HEAD_MAX_AXES)(*self.sections), eps, weight_offset, ptr(w_q),
+                              ptr(w_k), ptr(self.inv_freq))
+        self.ref = ctypes.byref(self.c)
+
+    def check(self, q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None):
+        """(device, tokens, heads and row strides of q and k, address of the positions)."""
+        some = q if q is not None else k
+        if some is None or not some.is_cuda or (self.device is not None and some.device != self.device):
+            raise NQError(NQ_ERR_INVALID_ARG, "q or k must be given, on the weights' device")
+        dev, tokens = some.device, some.shape[0] if some.dim() == 3 else -1
+        qs = _head_rows(q, "q", self.act_dtype, None, self.head_dim, dev) if q is not None else 0
+        ks = _head_rows(k, "k", self.act_dtype, None, self.head_dim, dev) if k is not None else 0
+        if k is not None and k.shape[0] != tokens:
+            raise NQError(NQ_ERR_INVALID_ARG, f"q of {tokens} tokens, k of {k.shape[0]}")
+        pp = None
+        if self.inv_freq is not None:
+            shape = positions.shape if positions is not None else None
+            if shape is None or positions.dtype != torch.int64 or positions.device != dev or \
+                    not positions.is_contiguous() or (shape != (self.axes, tokens) and
+                                                      not (self.axes == 1 and shape == (tokens,))):
+                raise NQError(NQ_ERR_INVALID_ARG, f"positions must be a contiguous int64 tensor of shape ({self.axes}, "
+                                                  f"{tokens}) on {dev}")
+            pp = positions.data_ptr()
+        return dev, tokens, q.shape[1] if q is not None else 0, qs, k.shape[1] if k is not None else 0, ks, pp
+
+
+def head_norm(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor | None, norm: HeadNorm,
+              inplace: bool = False, stream=None):
+    """(q', k'): norm and rotation of the heads of q and k, (tokens, heads, head_dim) each
+    (either may be None; rows may be parts of wider ones), at positions (tokens,) or
+    (axes, tokens) int64.  inplace writes over contiguous q and k."""
+    dev, tokens, qh, qs, kh, ks, pp = norm.check(q, k, positions)
+    if inplace and not all(t is None or t.is_contiguous() for t in (q, k)):
+        raise NQError(NQ_ERR_INVALID_ARG, "inplace needs contiguous q and k")
+
+    def call(s):
+        qo, ko = (t if t is None or inplace else torch.empty(t.shape, dtype=t.dtype, device=dev) for t in (q, k))
+        _check(lib().nq_head_norm_fwd(norm.ref, tokens, q.data_ptr() if qh else None, qs, qh,
+                                      k.data_ptr() if kh else None, ks, kh, pp, qo.data_ptr() if qh else None,
+                                      ko.data_ptr() if kh else None, s))
+        return qo, ko
+
+    return _on_stream(dev, stream, call)
+
+
+def head_norm_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None, norm: HeadNorm,
+                    cache: KvCache, slots: torch.Tensor, stream=None) -> torch.Tensor:
+    """q' of head_norm, with k' and v written to the cache's slots in the same launch: what
+    head_norm and then kv_write(k', v, cache, slots) leave there, bit for bit."""
+    dev, tokens, qh, qs, kh, ks, pp = norm.check(q, k, positions)
+    vs = _head_rows(v, "v", norm.act_dtype, kh, norm.head_dim, dev)
+    if cache.device != dev or cache.heads != kh or v.shape[0] != tokens:
+        raise NQError(NQ_ERR_INVALID_ARG, f"k and v must have the cache's {cache.heads} heads, on {cache.device}, and "
+                                          f"{tokens} tokens")
+    _kv_slots(slots, tokens, dev)
+
+    def call(s):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _check(lib().nq_head_norm_kv_write(norm.ref, tokens, q.data_ptr(), qs, qh, k.data_ptr(), ks, v.data_ptr(), vs,
+                                           pp, cache.ref, slots.data_ptr(), qo.data_ptr(), s))
+        return qo
+
+    return _on_stream(dev, stream, call)
+
+
+def head_norm_backward(dq: torch.Tensor | None, dk: torch.Tensor | None, q: torch.Tensor | None,
+                       k: torch.Tensor | None, positions: torch.Tensor | None, norm: HeadNorm, inplace: bool = False,
+                       workspace: torch.Tensor | None = None, stream=None) -> dict:
+    """Gradients of head_norm from dq and dk, those of q' and k' (contiguous), with q, k and
+    positions as there.  Returns a dict of "dq" and "dk" (written over the given ones with
+    inplace) for the q and k that are given and, where the norm has the weight, "dw_q" and
+    "dw_k" (fp32, sums over tokens and heads)."""
+    dev, tokens, qh, qs, kh, ks, pp = norm.check(q, k, positions)
+    if (dq is None) != (q is None) or (dk is None) != (k is None):
+        raise NQError(NQ_ERR_INVALID_ARG, "a gradient for each of q and k that is given")
+    for d, t, name in ((dq, q, "dq"), (dk, k, "dk")):
+        if t is not None:
+            _gpu_tensor(d, name, norm.act_dtype, t.shape, dev)
+    if workspace is not None:
+        _scratch(workspace, dev)
+
+    def call(s):
+        out = {}
+        for name, d in (("dq", dq), ("dk", dk)):
+            if d is not None:
+                out[name] = d if inplace else torch.empty_like(d)
+        for name, w, t in (("dw_q", norm.w_q, q), ("dw_k", norm.w_k, k)):
+            if w is not None and t is not None:
+                out[name] = torch.empty(norm.head_dim, dtype=torch.float32, device=dev)
+        ptr = lambda key: out[key].data_ptr() if key in out else None  # noqa: E731
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(max(int(lib().nq_head_norm_workspace_bytes(norm.ref, tokens)), 256), dtype=torch.uint8,
+                             device=dev)
+        _check(lib().nq_head_norm_bwd(norm.ref, tokens, dq.data_ptr() if qh else None, dk.data_ptr() if kh else None,
+                                      q.data_ptr() if qh else None, qs, qh, k.data_ptr() if kh else None, ks, kh, pp,
+                                      ptr("dq"), ptr("dk"), ptr("dw_q"), ptr("dw_k"), ws.data_ptr(), ws.numel(), s))
         return out
 
     return _on_stream(dev, stream, call)

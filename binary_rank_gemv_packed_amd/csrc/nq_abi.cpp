@@ -1057,6 +1057,435 @@ nq_status nq_block_norm_bwd(const nq_block_norm* N, int32_t rows, const void* dx
   return ok();
 }
 
+// ------------------------------------------------------------------ cache of keys and values
+namespace {
+
+constexpr int32_t KV_MAX_PAGES = 1 << 24, KV_MAX_HEADS = 128, KV_MAX_Q_HEADS = 1024;
+constexpr int64_t MAX_STRIDE = (int64_t)1 << 40;  // elements
+
+bool kv_shape_ok(int32_t heads, int32_t head_dim, int32_t page, int32_t kind) {
+  const bool dim = head_dim == 64 || head_dim == 96 || head_dim == 128 || head_dim == 192 || head_dim == 256;
+  return heads >= 1 && heads <= KV_MAX_HEADS && dim && page >= 16 && page <= 1024 && page % 16 == 0 &&
+         kind >= NQ_KV_BF16 && kind <= NQ_KV_INT4;
+}
+
+nq_status check_cache(const nq_kv_cache* C) {
+  if (!C) return fail(NQ_ERR_INVALID_ARG, "cache is NULL");
+  if (C->pages < 1 || C->pages > KV_MAX_PAGES)
+    return fail(NQ_ERR_INVALID_ARG, "pages %d out of range 1..%d", C->pages, KV_MAX_PAGES);
+  if (!kv_shape_ok(C->heads, C->head_dim, C->page, C->kind))
+    return fail(NQ_ERR_INVALID_ARG,
+                "heads %d (1..%d), head_dim %d (64, 96, 128, 192 or 256), page %d (a multiple of 16, 16..1024) or kind "
+                "%d out of range", C->heads, KV_MAX_HEADS, C->head_dim, C->page, C->kind);
+  if (!C->data || misaligned(C->data, 256)) return fail(NQ_ERR_INVALID_ARG, "cache data is NULL or not 256-byte aligned");
+  return NQ_OK;
+}
+
+nq::KvLayout layout_of(const nq_kv_cache* C) {
+  return nq::kv_layout(C->pages, C->heads, C->head_dim, C->page, C->kind);
+}
+
+size_t cache_bytes(const nq_kv_cache* C) { return layout_of(C).page_bytes * (size_t)C->pages; }
+
+// Rows of `width` elements `stride` apart: what they span.
+size_t rows_bytes(int32_t rows, int64_t stride, int64_t width, int elem) {
+  return rows ? ((size_t)(rows - 1) * stride + width) * elem : 0;
+}
+
+nq_status check_rows(const char* name, const void* p, int32_t rows, int64_t stride, int64_t width, int elem) {
+  if (!p) return fail(NQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (misaligned(p, elem)) return fail(NQ_ERR_INVALID_ARG, "%s is not aligned to its element size", name);
+  if (stride > MAX_STRIDE || (rows > 1 && stride < width))
+    return fail(NQ_ERR_INVALID_ARG, "%s: rows of %lld elements are %lld apart", name, (long long)width, (long long)stride);
+  return NQ_OK;
+}
+
+nq_status check_tokens(int32_t tokens) {
+  if (tokens < 0 || tokens > MAX_BATCH) return fail(NQ_ERR_INVALID_ARG, "tokens %d out of range 0..%d", tokens, MAX_BATCH);
+  return NQ_OK;
+}
+
+nq::KvArgs kv_args(const nq_kv_cache* C, int32_t tokens, int32_t dtype, const int64_t* slots, nq_stream_t stream) {
+  nq::KvArgs a{};
+  a.cache = layout_of(C);
+  a.data = static_cast<uint8_t*>(C->data);
+  a.tokens = tokens;
+  a.dtype = dtype;
+  a.slots = slots;
+  a.stream = reinterpret_cast<hipStream_t>(stream);
+  return a;
+}
+
+}  // namespace
+
+size_t nq_kv_page_bytes(int32_t heads, int32_t head_dim, int32_t page, int32_t kind) {
+  if (!kv_shape_ok(heads, head_dim, page, kind)) return 0;
+  return nq::kv_layout(1, heads, head_dim, page, kind).page_bytes;
+}
+
+nq_status nq_kv_write(const nq_kv_cache* C, int32_t tokens, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int32_t dtype, const int64_t* slots, nq_stream_t stream) {
+  nq_status st = check_cache(C);
+  if (!st) st = check_tokens(tokens);
+  if (st) return st;
+  const int eb = act_bytes(dtype);
+  if (!eb) return fail(NQ_ERR_INVALID_ARG, "dtype %d is not NQ_BF16 or NQ_F32", dtype);
+  if (tokens == 0) return ok();
+  const int64_t width = (int64_t)C->heads * C->head_dim;
+  st = check_rows("k", k, tokens, k_stride, width, eb);
+  if (!st) st = check_rows("v", v, tokens, v_stride, width, eb);
+  if (st) return st;
+  if (!slots || misaligned(slots, 8)) return fail(NQ_ERR_INVALID_ARG, "slots is NULL or not aligned to its element size");
+  const Span outs[] = {{C->data, cache_bytes(C), "the cache"}};
+  const Span ins[] = {{k, rows_bytes(tokens, k_stride, width, eb), "k"}, {v, rows_bytes(tokens, v_stride, width, eb), "v"},
+                      {slots, (size_t)tokens * 8, "slots"}};
+  st = check_apart(outs, 1, ins, 3, -1);
+  if (st) return st;
+  nq::KvArgs a = kv_args(C, tokens, dtype, slots, stream);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  (void)hipGetLastError();
+  const hipError_t e = nq::kv_write(a);
+  if (e != hipSuccess) return hip_fail(e, "cache write launch");
+  return ok();
+}
+
+nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots, void* k_out, void* v_out,
+                     int32_t dtype, nq_stream_t stream) {
+  nq_status st = check_cache(C);
+  if (!st) st = check_tokens(tokens);
+  if (st) return st;
+  const int eb = act_bytes(dtype);
+  if (!eb) return fail(NQ_ERR_INVALID_ARG, "dtype %d is not NQ_BF16 or NQ_F32", dtype);
+  if (tokens == 0) return ok();
+  const int64_t width = (int64_t)C->heads * C->head_dim;
+  st = check_rows("k_out", k_out, tokens, width, width, eb);
+  if (!st) st = check_rows("v_out", v_out, tokens, width, width, eb);
+  if (st) return st;
+  if (!slots || misaligned(slots, 8)) return fail(NQ_ERR_INVALID_ARG, "slots is NULL or not aligned to its element size");
+  const size_t bytes = (size_t)tokens * width * eb;
+  const Span outs[] = {{k_out, bytes, "k_out"}, {v_out, bytes, "v_out"}};
+  const Span ins[] = {{C->data, cache_bytes(C), "the cache"}, {slots, (size_t)tokens * 8, "slots"}};
+  st = check_apart(outs, 2, ins, 2, -1);
+  if (st) return st;
+  nq::KvArgs a = kv_args(C, tokens, dtype, slots, stream);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  (void)hipGetLastError();
+  const hipError_t e = nq::kv_read(a);
+  if (e != hipSuccess) return hip_fail(e, "cache read launch");
+  return ok();
+}
+
+size_t nq_kv_attention_workspace_bytes(const nq_kv_cache* C) {
+  if (check_cache(C)) return 0;
+  return nq::attn_workspace(layout_of(C));
+}
+
+nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_t q_dtype, int32_t q_heads,
+                          const int32_t* table, int32_t table_width, const int32_t* lengths, int32_t max_length,
+                          int32_t window, float scale, void* y, int32_t y_dtype, void* workspace,
+                          size_t workspace_bytes, nq_stream_t stream) {
+  nq_status st = check_cache(C);
+  if (st) return st;
+  constexpr int32_t MAX_SEQUENCES = 1 << 16;
+  if (B < 0 || B >= MAX_SEQUENCES) return fail(NQ_ERR_INVALID_ARG, "B %d out of range 0..%d", B, MAX_SEQUENCES - 1);
+  const int qb = act_bytes(q_dtype), yb = act_bytes(y_dtype);
+  if (!qb || !yb) return fail(NQ_ERR_INVALID_ARG, "q_dtype %d or y_dtype %d is not NQ_BF16 or NQ_F32", q_dtype, y_dtype);
+  if (q_heads < C->heads || q_heads > KV_MAX_Q_HEADS || q_heads % C->heads)
+    return fail(NQ_ERR_INVALID_ARG, "q_heads %d is not a multiple of the cache's %d up to %d", q_heads, C->heads, KV_MAX_Q_HEADS);
+  if (table_width < 1 || (int64_t)table_width * C->page > (int64_t)1 << 30)
+    return fail(NQ_ERR_INVALID_ARG, "a table of %d pages a sequence holds no or more than 2^30 tokens", table_width);
+  if (max_length < 0 || window < 0) return fail(NQ_ERR_INVALID_ARG, "max_length %d or window %d below zero", max_length, window);
+  if (!std::isfinite(scale)) return fail(NQ_ERR_INVALID_ARG, "scale must be finite");
+  if (B == 0) return ok();
+  const int64_t width = (int64_t)q_heads * C->head_dim;
+  st = check_rows("q", q, B, width, width, qb);
+  if (!st) st = check_rows("y", y, B, width, width, 16);
+  if (st) return st;
+  if (!table || !lengths || misaligned(table, 4) || misaligned(lengths, 4))
+    return fail(NQ_ERR_INVALID_ARG, "table or lengths is NULL or not aligned to its element size");
+  const size_t need = nq::attn_workspace(layout_of(C));
+  if (workspace_bytes < need)
+    return fail(NQ_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);
+  if (!workspace || misaligned(workspace, 256)) return fail(NQ_ERR_INVALID_ARG, "workspace is NULL or not 256-byte aligned");
+  const Span outs[] = {{y, (size_t)B * width * yb, "y"}, {workspace, need, "the workspace"}};
+  const Span ins[] = {{q, (size_t)B * width * qb, "q"},
+                      {C->data, cache_bytes(C), "the cache"},
+                      {table, (size_t)B * table_width * 4, "the table"},
+                      {lengths, (size_t)B * 4, "lengths"}};
+  st = check_apart(outs, 2, ins, 4, -1);
+  if (st) return st;
+  nq::AttnArgs a{};
+  a.cache = layout_of(C);
+  a.data = static_cast<const uint8_t*>(C->data);
+  a.B = B;
+  a.q_heads = q_heads;
+  a.q_dtype = q_dtype;
+  a.y_dtype = y_dtype;
+  a.q = q;
+  a.y = y;
+  a.table = table;
+  a.table_width = table_width;
+  a.lengths = lengths;
+  const int32_t holds = table_width * C->page;
+  a.max_length = max_length && max_length < holds ? max_length : holds;
+  a.window = window;
+  a.scale = scale;
+  a.part = static_cast<float*>(workspace);
+  a.stream = reinterpret_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  const hipError_t e = nq::attn_forward(a);
+  if (e != hipSuccess) return hip_fail(e, "attention launch");
+  return ok();
+}
+
+// ------------------------------------------------------------------ head norms
+namespace {
+
+nq_status check_heads(const nq_head_norm* N, int32_t tokens) {
+  if (!N) return fail(NQ_ERR_INVALID_ARG, "norm is NULL");
+  nq_status st = check_tokens(tokens);
+  if (st) return st;
+  if (N->head_dim < 2 || N->head_dim > NQ_HEAD_MAX_DIM || N->head_dim % 2)
+    return fail(NQ_ERR_INVALID_ARG, "head_dim %d is not even in 2..%d", N->head_dim, NQ_HEAD_MAX_DIM);
+  if (N->flags & ~(NQ_HEAD_NORM | NQ_HEAD_INTERLEAVED)) return fail(NQ_ERR_INVALID_ARG, "unknown flags %d", N->flags);
+  if (!act_bytes(N->act_dtype)) return fail(NQ_ERR_INVALID_ARG, "act_dtype %d is not NQ_BF16 or NQ_F32", N->act_dtype);
+  const int pb = any_bytes(N->param_dtype);
+  if (!pb) return fail(NQ_ERR_INVALID_ARG, "param_dtype %d is not NQ_F32, NQ_F16 or NQ_BF16", N->param_dtype);
+  if (N->rot < 0 || N->rot > N->head_dim || N->rot % 2)
+    return fail(NQ_ERR_INVALID_ARG, "rot %d is not even in 0..head_dim = %d", N->rot, N->head_dim);
+  if (!(N->flags & NQ_HEAD_NORM) && !N->rot) return fail(NQ_ERR_INVALID_ARG, "nothing to do: neither NQ_HEAD_NORM nor rot");
+  if (N->axes < 1 || N->axes > NQ_HEAD_MAX_AXES)
+    return fail(NQ_ERR_INVALID_ARG, "axes %d out of range 1..%d", N->axes, NQ_HEAD_MAX_AXES);
+  int64_t pairs = 0;
+  for (int i = 0; i < N->axes; i++) {
+    if (N->sections[i] < 0) return fail(NQ_ERR_INVALID_ARG, "section %d is negative", i);
+    pairs += N->sections[i];
+  }
+  if (pairs != N->rot / 2)
+    return fail(NQ_ERR_INVALID_ARG, "the sections hold %lld pairs, rot / 2 is %d", (long long)pairs, N->rot / 2);
+  if (!(N->eps > 0.0f) || !std::isfinite(N->eps)) return fail(NQ_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!std::isfinite(N->weight_offset)) return fail(NQ_ERR_INVALID_ARG, "weight_offset must be finite");
+  if (misaligned(N->w_q, pb) || misaligned(N->w_k, pb) || misaligned(N->inv_freq, 8))
+    return fail(NQ_ERR_INVALID_ARG, "w_q, w_k or inv_freq is not aligned to its element size");
+  if (N->rot && !N->inv_freq) return fail(NQ_ERR_INVALID_ARG, "rot without inv_freq");
+  return NQ_OK;
+}
+
+nq_status check_head_counts(int32_t q_heads, int32_t k_heads) {
+  if (q_heads < 0 || k_heads < 0 || q_heads > KV_MAX_Q_HEADS || k_heads > KV_MAX_Q_HEADS || q_heads + k_heads == 0)
+    return fail(NQ_ERR_INVALID_ARG, "q_heads %d and k_heads %d out of range 0..%d, or both zero", q_heads, k_heads, KV_MAX_Q_HEADS);
+  return NQ_OK;
+}
+
+nq_status check_positions(const nq_head_norm* N, const int64_t* positions) {
+  if (N->rot && (!positions || misaligned(positions, 8)))
+    return fail(NQ_ERR_INVALID_ARG, "positions is NULL or not aligned to its element size");
+  return NQ_OK;
+}
+
+nq::HeadArgs head_args(const nq_head_norm* N, int32_t tokens, const int64_t* positions, nq_stream_t stream) {
+  nq::HeadArgs a{};
+  a.tokens = tokens;
+  a.D = N->head_dim;
+  a.rot = N->rot;
+  a.axes = N->axes;
+  for (int i = 0, at = 0; i < 4; i++) {
+    if (i < N->axes) at += N->sections[i];
+    a.end[i] = i + 1 < N->axes ? at : N->head_dim;  // pairs behind the last axis: none
+  }
+  a.norm = (N->flags & NQ_HEAD_NORM) != 0;
+  a.interleaved = (N->flags & NQ_HEAD_INTERLEAVED) != 0;
+  a.act_dtype = N->act_dtype;
+  a.param_dtype = N->param_dtype;
+  a.eps = N->eps;
+  a.weight_offset = N->weight_offset;
+  a.w_q = N->w_q;
+  a.w_k = N->w_k;
+  a.inv_freq = N->inv_freq;
+  a.positions = positions;
+  a.stream = reinterpret_cast<hipStream_t>(stream);
+  return a;
+}
+
+// What the rows of a forward's or backward's inputs and parameters span.
+struct HeadSpans {
+  Span s[8];
+};
+HeadSpans param_spans(const nq_head_norm* N, int32_t tokens, const int64_t* positions) {
+  const size_t w = (size_t)N->head_dim * any_bytes(N->param_dtype);
+  return HeadSpans{{{N->w_q, w, "w_q"},
+                    {N->w_k, w, "w_k"},
+                    {N->rot ? N->inv_freq : nullptr, (size_t)N->rot * 4, "inv_freq"},
+                    {N->rot ? positions : nullptr, (size_t)tokens * N->axes * 8, "positions"}}};
+}
+
+// An output that is its own input: only where the input's rows are contiguous too.
+nq_status check_inplace(const char* name, const void* out, const void* in, int32_t tokens, int64_t stride, int64_t width) {
+  if (out == in && tokens > 1 && stride != width)
+    return fail(NQ_ERR_INVALID_ARG, "%s is its input, whose rows are not contiguous", name);
+  return NQ_OK;
+}
+
+}  // namespace
+
+nq_status nq_head_norm_fwd(const nq_head_norm* N, int32_t tokens, const void* q, int64_t q_stride, int32_t q_heads,
+                           const void* k, int64_t k_stride, int32_t k_heads, const int64_t* positions, void* q_out,
+                           void* k_out, nq_stream_t stream) {
+  nq_status st = check_heads(N, tokens);
+  if (!st) st = check_head_counts(q_heads, k_heads);
+  if (st || tokens == 0) return st ? st : ok();
+  const int eb = act_bytes(N->act_dtype);
+  const int64_t qw = (int64_t)q_heads * N->head_dim, kw = (int64_t)k_heads * N->head_dim;
+  st = check_positions(N, positions);
+  if (!st && q_heads) st = check_rows("q", q, tokens, q_stride, qw, eb);
+  if (!st && k_heads) st = check_rows("k", k, tokens, k_stride, kw, eb);
+  if (!st && q_heads) st = check_rows("q_out", q_out, tokens, qw, qw, eb);
+  if (!st && k_heads) st = check_rows("k_out", k_out, tokens, kw, kw, eb);
+  if (!st && q_heads) st = check_inplace("q_out", q_out, q, tokens, q_stride, qw);
+  if (!st && k_heads) st = check_inplace("k_out", k_out, k, tokens, k_stride, kw);
+  if (st) return st;
+  HeadSpans in = param_spans(N, tokens, positions);
+  in.s[4] = {q_heads && q != q_out ? q : nullptr, rows_bytes(tokens, q_stride, qw, eb), "q"};
+  in.s[5] = {k_heads && k != k_out ? k : nullptr, rows_bytes(tokens, k_stride, kw, eb), "k"};
+  const Span outs[] = {{q_heads ? q_out : nullptr, (size_t)tokens * qw * eb, "q_out"},
+                       {k_heads ? k_out : nullptr, (size_t)tokens * kw * eb, "k_out"}};
+  st = check_apart(outs, 2, in.s, 6, -1);
+  if (st) return st;
+  nq::HeadArgs a = head_args(N, tokens, positions, stream);
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_heads = q_heads;
+  a.k_heads = k_heads;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  (void)hipGetLastError();
+  const hipError_t e = nq::head_forward(a);
+  if (e != hipSuccess) return hip_fail(e, "head norm launch");
+  return ok();
+}
+
+nq_status nq_head_norm_kv_write(const nq_head_norm* N, int32_t tokens, const void* q, int64_t q_stride,
+                                int32_t q_heads, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int64_t* positions, const nq_kv_cache* C, const int64_t* slots, void* q_out,
+                                nq_stream_t stream) {
+  nq_status st = check_heads(N, tokens);
+  if (!st) st = check_cache(C);
+  if (!st) st = check_head_counts(q_heads, C->heads);
+  if (st) return st;
+  if (C->head_dim != N->head_dim)
+    return fail(NQ_ERR_INVALID_ARG, "heads of %d channels, a cache of %d", N->head_dim, C->head_dim);
+  if (tokens == 0) return ok();
+  const int eb = act_bytes(N->act_dtype);
+  const int64_t qw = (int64_t)q_heads * N->head_dim, kw = (int64_t)C->heads * N->head_dim;
+  st = check_positions(N, positions);
+  if (!st && q_heads) st = check_rows("q", q, tokens, q_stride, qw, eb);
+  if (!st) st = check_rows("k", k, tokens, k_stride, kw, eb);
+  if (!st) st = check_rows("v", v, tokens, v_stride, kw, eb);
+  if (!st && q_heads) st = check_rows("q_out", q_out, tokens, qw, qw, eb);
+  if (!st && q_heads) st = check_inplace("q_out", q_out, q, tokens, q_stride, qw);
+  if (st) return st;
+  if (!slots || misaligned(slots, 8)) return fail(NQ_ERR_INVALID_ARG, "slots is NULL or not aligned to its element size");
+  HeadSpans in = param_spans(N, tokens, positions);
+  in.s[4] = {q_heads && q != q_out ? q : nullptr, rows_bytes(tokens, q_stride, qw, eb), "q"};
+  in.s[5] = {k, rows_bytes(tokens, k_stride, kw, eb), "k"};
+  in.s[6] = {v, rows_bytes(tokens, v_stride, kw, eb), "v"};
+  in.s[7] = {slots, (size_t)tokens * 8, "slots"};
+  // q written in place is an input of nothing else: the cache must not lie on it either
+  const Span outs[] = {{q_heads ? q_out : nullptr, (size_t)tokens * qw * eb, "q_out"}, {C->data, cache_bytes(C), "the cache"}};
+  st = check_apart(outs, 2, in.s, 8, -1);
+  if (st) return st;
+  nq::HeadArgs a = head_args(N, tokens, positions, stream);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_heads = q_heads;
+  a.k_heads = C->heads;
+  a.q_out = q_out;
+  a.cache = layout_of(C);
+  a.data = static_cast<uint8_t*>(C->data);
+  a.slots = slots;
+  (void)hipGetLastError();
+  const hipError_t e = nq::head_write(a);
+  if (e != hipSuccess) return hip_fail(e, "head norm and cache write launch");
+  return ok();
+}
+
+size_t nq_head_norm_workspace_bytes(const nq_head_norm* N, int32_t tokens) {
+  if (check_heads(N, tokens)) return 0;
+  return nq::align_up((size_t)nq::head_bwd_parts(tokens) * 2 * N->head_dim * 4, 256);
+}
+
+nq_status nq_head_norm_bwd(const nq_head_norm* N, int32_t tokens, const void* dq_out, const void* dk_out,
+                           const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride,
+                           int32_t k_heads, const int64_t* positions, void* dq, void* dk, float* dw_q, float* dw_k,
+                           void* workspace, size_t workspace_bytes, nq_stream_t stream) {
+  nq_status st = check_heads(N, tokens);
+  if (!st) st = check_head_counts(q_heads, k_heads);
+  if (st) return st;
+  const bool norm = (N->flags & NQ_HEAD_NORM) != 0;
+  if ((dw_q && !(norm && N->w_q)) || (dw_k && !(norm && N->w_k)))
+    return fail(NQ_ERR_INVALID_ARG, "dw_q or dw_k asked for without NQ_HEAD_NORM and its weight");
+  const bool sums = dw_q || dw_k;
+  if (!tokens && !sums) return ok();
+  const int eb = act_bytes(N->act_dtype);
+  const int64_t qw = (int64_t)q_heads * N->head_dim, kw = (int64_t)k_heads * N->head_dim;
+  if (misaligned(dw_q, 4) || misaligned(dw_k, 4))
+    return fail(NQ_ERR_INVALID_ARG, "dw_q or dw_k is not aligned to its element size");
+  if (tokens) {
+    st = check_positions(N, positions);
+    if (!st && q_heads && norm) st = check_rows("q", q, tokens, q_stride, qw, eb);
+    if (!st && k_heads && norm) st = check_rows("k", k, tokens, k_stride, kw, eb);
+    if (!st && q_heads) st = check_rows("dq_out", dq_out, tokens, qw, qw, eb);
+    if (!st && k_heads) st = check_rows("dk_out", dk_out, tokens, kw, kw, eb);
+    if (!st && q_heads) st = check_rows("dq", dq, tokens, qw, qw, eb);
+    if (!st && k_heads) st = check_rows("dk", dk, tokens, kw, kw, eb);
+    if (st) return st;
+  }
+  const size_t need = sums ? nq_head_norm_workspace_bytes(N, tokens) : 0;
+  if (workspace_bytes < need)
+    return fail(NQ_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes, need);
+  if (need && !workspace) return fail(NQ_ERR_INVALID_ARG, "workspace is NULL");
+  if (misaligned(workspace, 256)) return fail(NQ_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  HeadSpans in = param_spans(N, tokens, positions);
+  const size_t q_bytes = (size_t)tokens * qw * eb, k_bytes = (size_t)tokens * kw * eb, w = (size_t)N->head_dim * 4;
+  in.s[4] = {norm && q_heads ? q : nullptr, rows_bytes(tokens, q_stride, qw, eb), "q"};
+  in.s[5] = {norm && k_heads ? k : nullptr, rows_bytes(tokens, k_stride, kw, eb), "k"};
+  in.s[6] = {q_heads && dq_out != dq ? dq_out : nullptr, q_bytes, "dq_out"};
+  in.s[7] = {k_heads && dk_out != dk ? dk_out : nullptr, k_bytes, "dk_out"};
+  const Span outs[] = {{tokens && q_heads ? dq : nullptr, q_bytes, "dq"}, {tokens && k_heads ? dk : nullptr, k_bytes, "dk"},
+                       {dw_q, w, "dw_q"},                                 {dw_k, w, "dw_k"},
+                       {need ? workspace : nullptr, need, "the workspace"}};
+  st = check_apart(outs, 5, in.s, 8, -1);
+  if (st) return st;
+  nq::HeadArgs a = head_args(N, tokens, positions, stream);
+  a.q = q;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_heads = q_heads;
+  a.k_heads = k_heads;
+  a.q_out = dq;
+  a.k_out = dk;
+  a.dq = dq_out;
+  a.dk = dk_out;
+  a.dw_q = dw_q;
+  a.dw_k = dw_k;
+  a.part = need ? static_cast<float*>(workspace) : nullptr;
+  (void)hipGetLastError();
+  const hipError_t e = nq::head_backward(a);
+  if (e != hipSuccess) return hip_fail(e, "head norm backward launch");
+  return ok();
+}
+
 double nq_bits_per_weight(int32_t m, int32_t n, int32_t r, int32_t scale_bits) {
   if (m < 1 || n < 1 || r < 0 || scale_bits < 0) return -1.0;
   return ((double)r * ((double)m + n) + (double)scale_bits * ((double)m + n + r)) / ((double)m * n);

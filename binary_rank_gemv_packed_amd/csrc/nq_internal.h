@@ -5,6 +5,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include "nq_kv.h"
+
 namespace nq {
 
 hipError_t launch_pack(const int8_t* M, int R, int C, long long ld_row, long long ld_col, uint32_t* out,
@@ -233,5 +235,77 @@ struct NormArgs {
 int norm_bwd_parts(int rows);
 hipError_t norm_forward(const NormArgs& a);
 hipError_t norm_backward(const NormArgs& a);
+
+// Paged cache of keys and values (nq_kv.hip): `tokens` rows of k and v (strides in
+// elements) to or from their slots.
+struct KvArgs {
+  KvLayout cache;
+  uint8_t* data;
+  int tokens, dtype;
+  const int64_t* slots;
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;
+  void* k_out;
+  void* v_out;
+  hipStream_t stream;
+};
+hipError_t kv_write(const KvArgs& a);
+hipError_t kv_read(const KvArgs& a);
+
+// Norms and rotation of heads (nq_head.hip): rows of q (q_heads) and k (k_heads)
+// of `tokens` tokens -> q_out, k_out, or with a cache q_out and the slots' keys and
+// values; backward: gradients dq, dk of the outputs -> dq_out, dk_out and, through
+// part, dw_q and dw_k.
+constexpr int HEAD_MAX_DIM = 512;
+struct HeadArgs {
+  int tokens, D, rot, axes;
+  int end[4];  // the pair behind each axis's last one
+  bool norm, interleaved;
+  int act_dtype, param_dtype;
+  float eps, weight_offset;
+  const void* w_q;
+  const void* w_k;
+  const double* inv_freq;
+  const int64_t* positions;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  int q_heads, k_heads;
+  void* q_out;
+  void* k_out;
+  KvLayout cache;
+  uint8_t* data;
+  const int64_t* slots;
+  const void* dq;
+  const void* dk;
+  float* dw_q;
+  float* dw_k;
+  float* part;  // [head_bwd_parts(tokens)][2][D]
+  hipStream_t stream;
+};
+int head_bwd_parts(int tokens);
+hipError_t head_forward(const HeadArgs& a);
+hipError_t head_write(const HeadArgs& a);
+hipError_t head_backward(const HeadArgs& a);
+
+// One token's attention over the paged cache (nq_attn.hip).
+struct AttnArgs {
+  KvLayout cache;
+  const uint8_t* data;
+  int B, q_heads, q_dtype, y_dtype;
+  const void* q;
+  void* y;
+  const int32_t* table;
+  int table_width;
+  const int32_t* lengths;
+  int max_length, window;
+  float scale;
+  float* part;
+  hipStream_t stream;
+};
+size_t attn_workspace(const KvLayout& l);
+hipError_t attn_forward(const AttnArgs& a);
 
 }  // namespace nq

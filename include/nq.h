@@ -1,8 +1,10 @@
 /*
  * nq.h -- C ABI of libnq: linear layers whose weight is a low-rank product of
  * bit-packed sign matrices and diagonal scales, on AMD Instinct MI355X (gfx950),
- * and what a model calls beside them: linears with 4-bit weights, and the norms
- * between its blocks.
+ * and what a model calls beside them: linears with 4-bit weights, the norms
+ * between its blocks, and what stands between the q, k, v linears and the output
+ * linear of a block: norms and rotation of heads, a paged cache of keys and values, one
+ * token's attention over it.
  *
  * The operation (hardwired.dev NanoQuant article, section "Jak NanoQuant
  * funguje": the weight is factored into sign matrices and diagonal scales;
@@ -381,6 +383,135 @@ nq_status nq_block_norm_bwd(const nq_block_norm* N, int32_t rows, const void* dx
                             const void* h_out, const void* y, const void* gate_rows, const float* stats, void* dh,
                             void* dy, void* dgate_rows, float* dw_post, float* dw_pre, float* dgate, void* workspace,
                             size_t workspace_bytes, nq_stream_t stream);
+
+/* ------------------------------------------------------------------ cache of keys and values
+ * Keys and values of many sequences in pages of `page` slots, a slot holding one
+ * token's keys and values of all heads.  Slot s is place s % page of page s / page;
+ * which slots a sequence has is the caller's (a table of pages, below).  kind says how
+ * a value x is held:
+ *
+ *     NQ_KV_BF16   bf16(x)
+ *     NQ_KV_INT8   s c, s = bf16(max |x| / 127) over the head's channels, c = x / s to the
+ *                  nearest, ties to even
+ *     NQ_KV_INT4   s c, s = bf16(max |x| / 7) over each 32 channels of the head
+ *
+ * A group (head or 32 channels) with an infinity or a NaN reads back as NaN, one
+ * whose scale rounds to zero (below 2^-134 times 127 or 7) as zeros.  The layout is the kernels' own (tiles of 16
+ * slots in the order of the attention's matrix operands); a page is position
+ * independent and may be copied as bytes. */
+typedef enum { NQ_KV_BF16 = 0, NQ_KV_INT8 = 1, NQ_KV_INT4 = 2 } nq_kv_kind;
+typedef struct {
+  int32_t pages;    /* 1 <= pages <= 2^24                              */
+  int32_t heads;    /* key heads, 1..128                               */
+  int32_t head_dim; /* 64, 96, 128, 192 or 256, of keys and values     */
+  int32_t page;     /* slots of a page: a multiple of 16, 16..1024     */
+  int32_t kind;     /* nq_kv_kind                                      */
+  void* data;       /* device, pages * nq_kv_page_bytes(), 256-byte aligned, owned by the caller */
+} nq_kv_cache;
+
+/* Bytes of one page; 0 for invalid arguments. */
+size_t nq_kv_page_bytes(int32_t heads, int32_t head_dim, int32_t page, int32_t kind);
+
+/* Writes `tokens` tokens: row t of k and v (heads x head_dim contiguous, rows
+ * k_stride and v_stride elements apart, dtype NQ_BF16 or NQ_F32, aligned to the element) to slot
+ * slots[t].  Slots outside the cache (negative ones, say) are left out; a slot
+ * given twice holds either token, or parts of both.  Nothing else of a page
+ * changes.  Asynchronous on `stream`, capturable; tokens == 0 launches nothing. */
+nq_status nq_kv_write(const nq_kv_cache* C, int32_t tokens, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int32_t dtype, const int64_t* slots, nq_stream_t stream);
+
+/* Reads slots back: k_out and v_out (tokens x heads x head_dim, contiguous) are
+ * the held values, rounded once to dtype; zeros for a slot outside the cache. */
+nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots, void* k_out, void* v_out,
+                     int32_t dtype, nq_stream_t stream);
+
+/* Attention of one new token a sequence over the cache:
+ *
+ *     y[b,h] = sum_t softmax_t(scale q[b,h] . k_t) v_t,   t = max(0, n - window) .. n - 1, n = lengths[b]
+ *
+ * with keys and values of head h / (q_heads / heads); window 0 sees all tokens.
+ * Token t of sequence b lies in slot t % page of page table[b * table_width + t / page].
+ *   q, y    : device, B x q_heads x head_dim, q_dtype and y_dtype NQ_BF16 or NQ_F32;
+ *             y 16-byte aligned; q_heads a multiple of heads, up to 1024
+ *   lengths : device, B: tokens of each sequence, the new one (already written) among them.
+ *             0 gives zeros.  At most max_length, which is what the host knows of them (0, or
+ *             more than the table holds: table_width * page); a length outside 0..max_length
+ *             makes its sequence's outputs NaN
+ *   table   : device; entries of pages without a token that is seen are not read; a page
+ *             outside the cache, where one is, makes outputs of its sequence NaN and is not read
+ *   workspace : device, >= nq_kv_attention_workspace_bytes(C), 256-byte aligned; no initial contents
+ * Scores, softmax statistics and sums are fp32; weights of the softmax are rounded to
+ * bf16 (2^-9) for bf16 q and y, else not.  What lies in slots that are not seen
+ * does not matter.  Asynchronous on `stream`, capturable (lengths and table are read by
+ * the kernels); calls that overlap in time need workspaces of their own; repeated calls
+ * give identical bits.  B == 0 launches nothing.  max_length chooses between one launch
+ * (up to 512) and a split over the length with a join. */
+size_t nq_kv_attention_workspace_bytes(const nq_kv_cache* C);
+nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_t q_dtype, int32_t q_heads,
+                          const int32_t* table, int32_t table_width, const int32_t* lengths, int32_t max_length,
+                          int32_t window, float scale, void* y, int32_t y_dtype, void* workspace,
+                          size_t workspace_bytes, nq_stream_t stream);
+
+/* ------------------------------------------------------------------ head norms
+ * Norm and rotation of the heads of queries and keys, in one launch.  For one head
+ * x (head_dim channels) of one token:
+ *
+ *     n = x r (w + weight_offset),  r = (mean x^2 + eps)^-1/2     (without NQ_HEAD_NORM: n = x)
+ *     (y_a, y_b) = (n_a cos p - n_b sin p, n_a sin p + n_b cos p)  for pair i < rot / 2,
+ *
+ * p = positions[axis of i][token] inv_freq[i], the other channels y = n.  Pair i is
+ * channels (i, i + rot / 2), with NQ_HEAD_INTERLEAVED (2i, 2i + 1).  Pairs go to the axes
+ * in order, sections[a] of them to axis a. */
+#define NQ_HEAD_NORM 1
+#define NQ_HEAD_INTERLEAVED 2
+#define NQ_HEAD_MAX_DIM 512
+#define NQ_HEAD_MAX_AXES 4
+typedef struct {
+  int32_t head_dim;    /* even, 2..NQ_HEAD_MAX_DIM                                    */
+  int32_t flags;       /* NQ_HEAD_NORM, NQ_HEAD_INTERLEAVED; the norm or rot > 0      */
+  int32_t act_dtype;   /* of q, k, v, outputs and gradients: NQ_BF16 or NQ_F32        */
+  int32_t param_dtype; /* of w_q and w_k: NQ_F32, NQ_F16 or NQ_BF16                   */
+  int32_t rot;         /* rotated channels: even, 0..head_dim                         */
+  int32_t axes;        /* 1..NQ_HEAD_MAX_AXES                                         */
+  int32_t sections[NQ_HEAD_MAX_AXES]; /* their sum is rot / 2                         */
+  float eps;           /* > 0                                                         */
+  float weight_offset; /* finite                                                      */
+  const void* w_q;     /* device, head_dim values; NULL: 1 and no offset              */
+  const void* w_k;
+  const double* inv_freq; /* device, rot / 2; angles are formed in 64 bits            */
+} nq_head_norm;
+
+/* Forward.  Row t of q holds q_heads x head_dim contiguous elements, rows q_stride
+ * elements apart (a part of a wider linear's output), k likewise; q_out and k_out are
+ * contiguous and may be q and k themselves where those are.  q_heads or k_heads may be 0
+ * (the pointers may then be NULL).  positions: device, axes x tokens, below 2^53 in
+ * magnitude; may be NULL without rotation.  Arithmetic is fp32 but for the angles, each
+ * output is rounded once; a head whose sum of squares passes 3.4e38 gives zeros.
+ * Asynchronous on `stream`, capturable, no workspace; tokens == 0 launches nothing. */
+nq_status nq_head_norm_fwd(const nq_head_norm* N, int32_t tokens, const void* q, int64_t q_stride, int32_t q_heads,
+                           const void* k, int64_t k_stride, int32_t k_heads, const int64_t* positions, void* q_out,
+                           void* k_out, nq_stream_t stream);
+
+/* The same with k_out and v going to the cache: what nq_head_norm_fwd and then
+ * nq_kv_write(C, tokens, k_out, ..., v, ..., act_dtype, slots) leave there, bit for bit, in one
+ * launch.  k and v have C->heads heads of C->head_dim (= N->head_dim) channels. */
+nq_status nq_head_norm_kv_write(const nq_head_norm* N, int32_t tokens, const void* q, int64_t q_stride,
+                                int32_t q_heads, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const int64_t* positions, const nq_kv_cache* C, const int64_t* slots, void* q_out,
+                                nq_stream_t stream);
+
+/* Backward: dq_out and dk_out (contiguous, act_dtype) are the gradients of q_out and
+ * k_out, q and k the forward's inputs (unused without NQ_HEAD_NORM: may be NULL).  Writes
+ * dq and dk (contiguous; may be dq_out and dk_out themselves), and dw_q and dw_k (head_dim
+ * fp32 each, may be NULL; each needs its weight): sums over all tokens and heads, zeros for tokens == 0.
+ * The workspace is needed for these two only, no initial contents.  Sums are added in a
+ * fixed order: repeated calls give identical bits.  Asynchronous on `stream`, capturable;
+ * calls that overlap in time need workspaces of their own. */
+size_t nq_head_norm_workspace_bytes(const nq_head_norm* N, int32_t tokens);
+nq_status nq_head_norm_bwd(const nq_head_norm* N, int32_t tokens, const void* dq_out, const void* dk_out,
+                           const void* q, int64_t q_stride, int32_t q_heads, const void* k, int64_t k_stride,
+                           int32_t k_heads, const int64_t* positions, void* dq, void* dk, float* dw_q, float* dw_k,
+                           void* workspace, size_t workspace_bytes, nq_stream_t stream);
 
 /* Average bits per original weight: (r(m+n) + scale_bits (m+n+r)) / (m n)
  * (hardwired.dev, sections "Jak NanoQuant funguje" and 'Co znamena
