@@ -1232,6 +1232,8 @@ nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_
   a.lengths = lengths;
   const int32_t holds = table_width * C->page;
   a.max_length = max_length && max_length < holds ? max_length : holds;
+  if ((int64_t)B * (a.max_length / 32 + 8) > INT32_MAX)
+    return fail(NQ_ERR_INVALID_ARG, "%d sequences of up to %d tokens: over 2^36 in all", B, a.max_length);
   a.window = window;
   a.scale = scale;
   a.part = static_cast<float*>(workspace);
