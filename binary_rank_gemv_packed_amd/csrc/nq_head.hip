@@ -38,96 +38,111 @@ struct HeadLanes {
   __device__ __forceinline__ int pair(int i) const { return (i / VEC * LG + m) * VEC + i % VEC; }
   __device__ __forceinline__ bool in(int i) const { return 2 * pair(i) < D; }
   __device__ __forceinline__ bool turned(int i) const { return pair(i) < half; }
+  __device__ __forceinline__ bool beside() const { return near || !turned(0); }  // members of pairs lie side by side
   // the channels of pair i
   __device__ __forceinline__ int first(int i) const { return near || !turned(i) ? 2 * pair(i) : pair(i); }
   __device__ __forceinline__ int second(int i) const { return near || !turned(i) ? 2 * pair(i) + 1 : pair(i) + half; }
 };
 
+// Four elements, and a lane's pairs of one head as they are stored, until get(): what
+// is asked for early takes no more registers than its bytes.
 template <typename T>
-__device__ __forceinline__ float head_get(const T* p, int k) {
-  return to_f32<T>(p[k]);
-}
+struct Four {
+  typedef typename std::conditional<sizeof(T) == 4, u32x4_at2, u32x2_at2>::type word;
+  word u;
+  __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const word*>(p); }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u[i]);
+    else if constexpr (std::is_same<T, _Float16>::value)
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)(u[i / 2] >> (16 * (i & 1))));
+    else return __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+  }
+};
 
-// Four elements from channel k on.
-__device__ __forceinline__ void four(const float* p, int k, float* v) {
-  const u32x4_at2 u = *reinterpret_cast<const u32x4_at2*>(p + k);
+template <typename T>
+__device__ __forceinline__ void put_four(T* p, const float* v) {
+  typename Four<T>::word u;
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = __uint_as_float(u[i]);
-}
-__device__ __forceinline__ void four(const uint16_t* p, int k, float* v) {
-  const u32x2_at2 u = *reinterpret_cast<const u32x2_at2*>(p + k);
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
-}
-__device__ __forceinline__ void four(const _Float16* p, int k, float* v) {
-  const u32x2_at2 u = *reinterpret_cast<const u32x2_at2*>(p + k);
-#pragma unroll
-  for (int i = 0; i < 4; i++) v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[i / 2] >> (16 * (i & 1))));
-}
-__device__ __forceinline__ void put_four(float* p, int k, const float* v) {
-  u32x4_at2 u;
-#pragma unroll
-  for (int i = 0; i < 4; i++) u[i] = __float_as_uint(v[i]);
-  *reinterpret_cast<u32x4_at2*>(p + k) = u;
-}
-__device__ __forceinline__ void put_four(uint16_t* p, int k, const float* v) {
-  u32x2_at2 u;
-#pragma unroll
-  for (int i = 0; i < 2; i++) u[i] = f32_to_bf16(v[2 * i]) | (uint32_t)f32_to_bf16(v[2 * i + 1]) << 16;
-  *reinterpret_cast<u32x2_at2*>(p + k) = u;
-}
-__device__ __forceinline__ void put_one(float* p, int k, float v) { p[k] = v; }
-__device__ __forceinline__ void put_one(uint16_t* p, int k, float v) { p[k] = f32_to_bf16(v); }
-
-// A lane's pairs of one head: v[i] and v[N + i] are the two members of pair i;
-// zeros behind D and where there is no head (p null).
-template <int VEC, int LG, int C, typename T>
-__device__ __forceinline__ void head_load(const HeadLanes<VEC, LG, C>& l, const T* p, float (&v)[2 * VEC * C]) {
-  constexpr int N = VEC * C;
-  if constexpr (VEC == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = 0.0f;
-    if (p && l.in(0)) {
-      const bool near = l.near || !l.turned(0);
-      float a[4], b[4];
-      four(p, l.first(0), a);
-      four(p, near ? l.first(0) + 4 : l.second(0), b);
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        v[i] = near ? (i < 2 ? a[2 * i] : b[2 * i - 4]) : a[i];
-        v[4 + i] = near ? (i < 2 ? a[2 * i + 1] : b[2 * i - 3]) : b[i];
-      }
-    }
+    for (int i = 0; i < 4; i++) u[i] = __float_as_uint(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      const bool on = p && l.in(i);
-      v[i] = on ? head_get(p, l.first(i)) : 0.0f;
-      v[N + i] = on ? head_get(p, l.second(i)) : 0.0f;
-    }
+    for (int i = 0; i < 2; i++) u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
   }
+  *reinterpret_cast<typename Four<T>::word*>(p) = u;
+}
+__device__ __forceinline__ void put_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put_one(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+
+// Element `k` of a row as a byte offset of 32 bits from the row's address, which is the
+// same for the wave.
+template <typename T>
+__device__ __forceinline__ T* head_at(T* row, uint32_t k) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
+  return reinterpret_cast<T*>(reinterpret_cast<byte*>(row) + k * (uint32_t)sizeof(T));
 }
 
+// A lane's pairs of one head that begins at element k of a row: zeros behind D and
+// where `on` is false.  get() gives v[i] and v[N + i], the two members of pair i.
+template <typename T, int VEC, int LG, int C>
+struct HeadRow {
+  static constexpr int N = VEC * C;
+  Four<T> a, b;           // VEC = 4
+  T one[VEC == 1 ? 2 * N : 1];
+  __device__ __forceinline__ void load(const HeadLanes<VEC, LG, C>& l, const T* row, uint32_t k, bool on) {
+    if constexpr (VEC == 4) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); i++) a.u[i] = b.u[i] = 0;
+      if (on && l.in(0)) {
+        a.load(head_at(row, k + l.first(0)));
+        b.load(head_at(row, k + (l.beside() ? l.first(0) + 4 : l.second(0))));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        one[i] = one[N + i] = T(0);
+        if (on && l.in(i)) {
+          one[i] = *head_at(row, k + l.first(i));
+          one[N + i] = *head_at(row, k + l.second(i));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(const HeadLanes<VEC, LG, C>& l, float (&v)[2 * N]) const {
+    if constexpr (VEC == 4) {
+      const bool beside = l.beside();
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[i] = beside ? (i < 2 ? a.get(2 * i) : b.get(2 * i - 4)) : a.get(i);
+        v[4 + i] = beside ? (i < 2 ? a.get(2 * i + 1) : b.get(2 * i - 3)) : b.get(i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * N; i++) v[i] = to_f32<T>(one[i]);
+    }
+  }
+};
+
 template <int VEC, int LG, int C, typename T>
-__device__ __forceinline__ void head_put(const HeadLanes<VEC, LG, C>& l, T* p, const float (&v)[2 * VEC * C]) {
+__device__ __forceinline__ void head_put(const HeadLanes<VEC, LG, C>& l, T* row, uint32_t k, const float (&v)[2 * VEC * C]) {
   constexpr int N = VEC * C;
   if constexpr (VEC == 4) {
     if (!l.in(0)) return;
-    const bool near = l.near || !l.turned(0);
+    const bool beside = l.beside();
     float a[4], b[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      a[i] = near ? v[(i & 1) * 4 + i / 2] : v[i];
-      b[i] = near ? v[(i & 1) * 4 + 2 + i / 2] : v[4 + i];
+      a[i] = beside ? v[(i & 1) * 4 + i / 2] : v[i];
+      b[i] = beside ? v[(i & 1) * 4 + 2 + i / 2] : v[4 + i];
     }
-    put_four(p, l.first(0), a);
-    put_four(p, near ? l.first(0) + 4 : l.second(0), b);
+    put_four(head_at(row, k + l.first(0)), a);
+    put_four(head_at(row, k + (beside ? l.first(0) + 4 : l.second(0))), b);
   } else {
 #pragma unroll
     for (int i = 0; i < N; i++)
       if (l.in(i)) {
-        put_one(p, l.first(i), v[i]);
-        put_one(p, l.second(i), v[N + i]);
+        put_one(head_at(row, k + l.first(i)), v[i]);
+        put_one(head_at(row, k + l.second(i)), v[N + i]);
       }
   }
 }
@@ -141,29 +156,56 @@ __device__ __forceinline__ void head_weights(const HeadLanes<VEC, LG, C>& l, con
     for (int i = 0; i < 2 * VEC * C; i++) v[i] = 1.0f;
     return;
   }
-  if (a.param_dtype == 0) head_load(l, static_cast<const float*>(w), v);
-  else if (a.param_dtype == 1) head_load(l, static_cast<const _Float16*>(w), v);
-  else head_load(l, static_cast<const uint16_t*>(w), v);
+  auto as = [&](auto t) {
+    HeadRow<decltype(t), VEC, LG, C> r;
+    r.load(l, static_cast<const decltype(t)*>(w), 0, true);
+    r.get(l, v);
+  };
+  if (a.param_dtype == 0) as(float{});
+  else if (a.param_dtype == 1) as(_Float16{});
+  else as(uint16_t{});
 #pragma unroll
   for (int i = 0; i < 2 * VEC * C; i++) v[i] += a.weight_offset;
 }
 
-// Sine and cosine of a lane's pairs at token t.
+// Orders a wave's accesses to shared memory between its lanes: LDS takes them in turn.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Cosine and sine of a lane's pairs at token t.  A wave's lanes form one pair's each
+// (those of one head's, where its slots would form them again for every head) and
+// pass them on through `shared`, the wave's own 2 x (LG VEC C) floats.
 template <int VEC, int LG, int C>
-__device__ __forceinline__ void head_angles(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, int t,
+__device__ __forceinline__ void head_angles(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, int t, float* shared,
                                             float (&c)[VEC * C], float (&s)[VEC * C]) {
+  constexpr int N = LG * VEC * C;
+#pragma unroll
+  for (int i = 0; i < (N + 63) / 64; i++) {
+    const int p = 64 * i + (threadIdx.x & 63);
+    if (p < l.half) {
+      const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
+      double u = (double)a.positions[(size_t)axis * a.tokens + t] * a.inv_freq[p] * 0.15915494309189533577;
+      u -= rint(u);
+      float sine, cosine;
+      sincospif((float)(2.0 * u), &sine, &cosine);
+      shared[p] = cosine;
+      shared[N + p] = sine;
+    }
+  }
+  wave_fence();
 #pragma unroll
   for (int i = 0; i < VEC * C; i++) {
     c[i] = 1.0f;
     s[i] = 0.0f;
     if (l.turned(i)) {
-      const int p = l.pair(i);
-      const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
-      double u = (double)a.positions[(size_t)axis * a.tokens + t] * a.inv_freq[p] * 0.15915494309189533577;
-      u -= rint(u);
-      sincospif((float)(2.0 * u), &s[i], &c[i]);
+      c[i] = shared[l.pair(i)];
+      s[i] = shared[N + l.pair(i)];
     }
   }
+  wave_fence();
 }
 
 // Sum over the LG lanes of a head, to each of them, in a fixed order.
@@ -185,82 +227,88 @@ __device__ __forceinline__ float round_to(float v, const uint16_t*) { return to_
 
 // ------------------------------------------------------------------ forward
 // A wave takes one token, or one of `parts` shares of a token's heads, so that the
-// angles are formed once for all of them; 64 / LG heads at a time, the next ones
-// asked for before the present ones are worked on.  Heads are numbered q, k, and with a
-// cache (KIND >= 0) v; keys and values then pass through shared memory to lanes of eight
-// channels each, as the cache's stores take them, after the rounding to T that k_out
-// would have had: the cache holds what a write of k_out would have put there.
+// angles are formed once for all of them; 64 / LG heads a round, the next round's
+// asked for before the present one's are worked on.  A round's heads are all queries, all
+// keys or, with a cache (KIND >= 0), all values.  Keys and values then pass through
+// shared memory to lanes of eight channels each, as the cache's stores take them, after
+// the rounding to T that k_out would have had: the cache holds what a write of k_out
+// would have put there.
 template <typename T, int VEC, int LG, int C, int KIND>
 __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
   constexpr int N = VEC * C, SLOTS = 64 / LG;
   constexpr bool WRITE = KIND >= 0;
-  __shared__ float turn_over[WRITE ? 4 * 512 : 1];
-  const int lane = threadIdx.x & 63, slot = lane / LG;
-  const long long job = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const bool on = job < (long long)a.tokens * parts;
-  const int t = on ? (int)(job / parts) : 0, part = (int)(job % parts);
+  __shared__ float turns[4][2 * LG * N];
+  __shared__ float turn_over[4][WRITE ? 512 : 1];
+  const int lane = threadIdx.x & 63, slot = lane / LG, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long job = (long long)blockIdx.x * 4 + wave;
+  if (job >= (long long)a.tokens * parts) return;
+  const int t = (int)(job / parts), part = (int)(job % parts);
   const HeadLanes<VEC, LG, C> l{lane % LG, a.D, a.rot / 2, a.interleaved};
-  const int heads = a.q_heads + a.k_heads * (WRITE ? 2 : 1), step = parts * SLOTS;
-  auto row = [&](int u) -> const T* {
-    if (!on || u >= heads) return nullptr;
-    if (u < a.q_heads) return static_cast<const T*>(a.q) + t * a.q_stride + (size_t)u * a.D;
-    u -= a.q_heads;
-    if (u < a.k_heads) return static_cast<const T*>(a.k) + t * a.k_stride + (size_t)u * a.D;
-    return static_cast<const T*>(a.v) + t * a.v_stride + (size_t)(u - a.k_heads) * a.D;
+  const int rq = (a.q_heads + SLOTS - 1) / SLOTS, rk = (a.k_heads + SLOTS - 1) / SLOTS, rounds = rq + (WRITE ? 2 : 1) * rk;
+  auto fetch = [&](HeadRow<T, VEC, LG, C>& to, int r) {
+    const int kind = (r >= rq) + (r >= rq + rk);
+    const T* row = static_cast<const T*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                   t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride);
+    const int u = (r - (kind ? rq : 0) - (kind == 2 ? rk : 0)) * SLOTS + slot;
+    to.load(l, row, u * a.D, u < (kind ? a.k_heads : a.q_heads));
   };
-  float next[2 * N], wq[2 * N], wk[2 * N], c[N], s[N];
-  head_load(l, row(part * SLOTS + slot), next);
+  HeadRow<T, VEC, LG, C> next;
+  fetch(next, part);
+  float wq[2 * N], wk[2 * N], c[N], s[N];
   head_weights(l, a, a.w_q, wq);
   head_weights(l, a, a.w_k, wk);
   KvPlace at{nullptr, 0, 0};
-  if (WRITE && on) at = kv_place(a.cache, a.data, a.slots[t]);
-  head_angles(l, a, t, c, s);
-  const int rounds = ceil_div(heads, step);  // the same in every wave, for the barriers
-  for (int k = 0; k < rounds; k++) {
-    const int u = part * SLOTS + slot + k * step;
+  if (WRITE) at = kv_place(a.cache, a.data, a.slots[t]);
+  head_angles(l, a, t, turns[wave], c, s);
+  for (int k = part; k < rounds; k += parts) {
+    const int kind = (k >= rq) + (k >= rq + rk), u = (k - (kind ? rq : 0) - (kind == 2 ? rk : 0)) * SLOTS + slot;
+    const bool on = u < (kind ? a.k_heads : a.q_heads);
     float x[2 * N], y[2 * N];
-#pragma unroll
-    for (int i = 0; i < 2 * N; i++) x[i] = next[i];
-    if (k + 1 < rounds) head_load(l, row(u + step), next);
-    const bool is_q = u < a.q_heads, is_v = WRITE && u >= a.q_heads + a.k_heads;
+    next.get(l, x);
+    if (k + parts < rounds) fetch(next, k + parts);
     float r = 1.0f;
-    if (a.norm) {
+    if (a.norm && !(WRITE && kind == 2)) {
       float ss = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2 * N; i++) ss = fmaf(x[i], x[i], ss);
       r = 1.0f / sqrtf(head_sum<LG>(ss) / (float)a.D + a.eps);
-    }
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      const float na = a.norm ? x[i] * r * (is_q ? wq[i] : wk[i]) : x[i];
-      const float nb = a.norm ? x[N + i] * r * (is_q ? wq[N + i] : wk[N + i]) : x[N + i];
-      const bool turn = l.turned(i);
-      y[i] = turn ? na * c[i] - nb * s[i] : na;
-      y[N + i] = turn ? na * s[i] + nb * c[i] : nb;
-    }
-    if (on && is_q) head_put(l, static_cast<T*>(a.q_out) + ((size_t)t * a.q_heads + u) * a.D, y);
-    if constexpr (!WRITE) {
-      if (on && !is_q && u < heads) head_put(l, static_cast<T*>(a.k_out) + ((size_t)t * a.k_heads + u - a.q_heads) * a.D, y);
+      for (int i = 0; i < 2 * N; i++) y[i] = x[i] * r * (kind ? wk[i] : wq[i]);
     } else {
-      __syncthreads();
-      float* mine = turn_over + (threadIdx.x >> 6) * 512 + slot * a.D;
+#pragma unroll
+      for (int i = 0; i < 2 * N; i++) y[i] = x[i];
+    }
+    if (!(WRITE && kind == 2)) {
+#pragma unroll
+      for (int i = 0; i < N; i++) {
+        const float na = y[i], nb = y[N + i];
+        const bool turn = l.turned(i);
+        y[i] = turn ? na * c[i] - nb * s[i] : na;
+        y[N + i] = turn ? na * s[i] + nb * c[i] : nb;
+      }
+    }
+    if (kind == 0) {
+      if (on) head_put(l, static_cast<T*>(a.q_out) + (size_t)t * a.q_heads * a.D, u * a.D, y);
+    } else if constexpr (!WRITE) {
+      if (on) head_put(l, static_cast<T*>(a.k_out) + (size_t)t * a.k_heads * a.D, u * a.D, y);
+    } else {
+      float* mine = turn_over[wave] + slot * a.D;
+      wave_fence();
 #pragma unroll
       for (int i = 0; i < N; i++)
         if (l.in(i)) {
-          mine[l.first(i)] = is_v ? x[i] : round_to(y[i], (const T*)nullptr);
-          mine[l.second(i)] = is_v ? x[N + i] : round_to(y[N + i], (const T*)nullptr);
+          mine[l.first(i)] = round_to(y[i], (const T*)nullptr);
+          mine[l.second(i)] = round_to(y[N + i], (const T*)nullptr);
         }
-      __syncthreads();
-      const bool held = on && !is_q && u < heads && 8 * l.m < a.D;
+      wave_fence();
+      const bool held = on && 8 * l.m < a.D;
       float e[8] = {};
       if (held) {
 #pragma unroll
         for (int i = 0; i < 8; i++) e[i] = mine[8 * l.m + i];
       }
-      const int head = u - a.q_heads - (is_v ? a.k_heads : 0);
-      // whole waves go through either store: its exchanges want every lane of a head
-      if (__any(held && !is_v)) kv_store<KIND, LG, false>(a.cache, at, held ? head : 0, l.m, held && !is_v, e);
-      if (__any(held && is_v)) kv_store<KIND, LG, true>(a.cache, at, held ? head : 0, l.m, held && is_v, e);
+      if (kind == 1) kv_store<KIND, LG, false>(a.cache, at, held ? u : 0, l.m, held, e);
+      else kv_store<KIND, LG, true>(a.cache, at, held ? u : 0, l.m, held, e);
     }
   }
 }
@@ -272,9 +320,9 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
 // a fixed order.
 template <typename T, int VEC, int LG, int C>
 __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
-  constexpr int N = VEC * C, SLOTS = 64 / LG;
-  __shared__ float red[16][HEAD_MAX_DIM];
-  const int lane = threadIdx.x & 63, slot = lane / LG, wave = threadIdx.x >> 6;
+  constexpr int N = VEC * C, SLOTS = 64 / LG, TURNS = 2 * LG * N;
+  __shared__ float red[16][TURNS > HEAD_MAX_DIM ? TURNS : HEAD_MAX_DIM];  // first the waves' angles, then their sums
+  const int lane = threadIdx.x & 63, slot = lane / LG, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const HeadLanes<VEC, LG, C> l{lane % LG, a.D, a.rot / 2, a.interleaved};
   float sums[2][2 * N];
 #pragma unroll
@@ -283,35 +331,35 @@ __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
   for (long long job = (long long)blockIdx.x * 16 + wave; job < jobs; job += (long long)gridDim.x * 16) {
     const int t = (int)(job / parts), part = (int)(job % parts);
     float c[N], s[N];
-    head_angles(l, a, t, c, s);
+    head_angles(l, a, t, red[wave], c, s);
 #pragma unroll
     for (int kind = 0; kind < 2; kind++) {
       const int heads = kind ? a.k_heads : a.q_heads, step = parts * SLOTS;
       const T* xs = kind ? static_cast<const T*>(a.k) + t * a.k_stride : static_cast<const T*>(a.q) + t * a.q_stride;
       const T* gs = static_cast<const T*>(kind ? a.dk : a.dq) + (size_t)t * heads * a.D;
       T* out = static_cast<T*>(kind ? a.k_out : a.q_out) + (size_t)t * heads * a.D;
-      float w[2 * N], x[2 * N], d[2 * N];
-      if (part * SLOTS < heads) {
-        const int u = part * SLOTS + slot;
-        head_load(l, a.norm && u < heads ? xs + (size_t)u * a.D : nullptr, x);
-        head_load(l, u < heads ? gs + (size_t)u * a.D : nullptr, d);
-        head_weights(l, a, kind ? a.w_k : a.w_q, w);
-      }
+      if (part * SLOTS >= heads) continue;
+      float w[2 * N];
+      HeadRow<T, VEC, LG, C> x, d;
+      int u = part * SLOTS + slot;
+      x.load(l, xs, u * a.D, a.norm && u < heads);
+      d.load(l, gs, u * a.D, u < heads);
+      head_weights(l, a, kind ? a.w_k : a.w_q, w);
       for (int base = part * SLOTS; base < heads; base += step) {
-        const int u = base + slot;
         float g[2 * N], n[2 * N];
+        x.get(l, n);
+        d.get(l, g);
+        const int v = u + step;
+        if (base + step < heads) {
+          x.load(l, xs, v * a.D, a.norm && v < heads);
+          d.load(l, gs, v * a.D, v < heads);
+        }
 #pragma unroll
         for (int i = 0; i < N; i++) {
+          const float da = g[i], db = g[N + i];
           const bool turn = l.turned(i);
-          g[i] = turn ? d[i] * c[i] + d[N + i] * s[i] : d[i];
-          g[N + i] = turn ? d[N + i] * c[i] - d[i] * s[i] : d[N + i];
-          n[i] = x[i];
-          n[N + i] = x[N + i];
-        }
-        if (base + step < heads) {
-          const int v = u + step;
-          head_load(l, a.norm && v < heads ? xs + (size_t)v * a.D : nullptr, x);
-          head_load(l, v < heads ? gs + (size_t)v * a.D : nullptr, d);
+          g[i] = turn ? da * c[i] + db * s[i] : da;
+          g[N + i] = turn ? db * c[i] - da * s[i] : db;
         }
         if (a.norm) {
           float ss = 0.0f, dot = 0.0f;
@@ -329,7 +377,8 @@ __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
 #pragma unroll
           for (int i = 0; i < 2 * N; i++) g[i] = r * (g[i] - n[i] * mean);
         }
-        if (u < heads) head_put(l, out + (size_t)u * a.D, g);
+        if (u < heads) head_put(l, out, u * a.D, g);
+        u = v;
       }
     }
   }
@@ -403,10 +452,11 @@ void head_dispatch(const HeadArgs& a, F f) {
 
 // Shares of a token's heads: enough that `waves` waves have work, at most one for
 // each round of heads.
-int head_parts(int tokens, int heads, int slots, int waves) {
-  const int most = ceil_div(heads, slots), want = ceil_div(waves, tokens);
-  return want < 1 ? 1 : want < most ? want : most;
+int head_parts(int tokens, int rounds, int waves) {
+  const int want = ceil_div(waves, tokens);
+  return ceil_div(rounds, ceil_div(rounds, want < rounds ? want : rounds));
 }
+constexpr int HEAD_WAVES = 6144;
 
 template <typename Kind>
 hipError_t head_launch(const HeadArgs& a, Kind) {
@@ -414,7 +464,9 @@ hipError_t head_launch(const HeadArgs& a, Kind) {
   head_dispatch(a, [&](auto t, auto vec, auto lg, auto c) {
     constexpr int LG = decltype(lg)::value, VEC = decltype(vec)::value, C = decltype(c)::value;
     if constexpr (KIND < 0 || VEC == 1 || LG < 64) {  // a cache's heads have 256 channels at most
-      const int parts = head_parts(a.tokens, a.q_heads + a.k_heads * (KIND < 0 ? 1 : 2), 64 / LG, 2048);
+      constexpr int SLOTS = 64 / LG;
+      const int rounds = ceil_div(a.q_heads, SLOTS) + ceil_div(a.k_heads, SLOTS) * (KIND < 0 ? 1 : 2);
+      const int parts = head_parts(a.tokens, rounds, HEAD_WAVES);
       const long long jobs = (long long)a.tokens * parts;
       hipLaunchKernelGGL((head_fwd_kernel<decltype(t), VEC, LG, C, KIND>), dim3((unsigned)((jobs + 3) / 4)), dim3(256), 0,
                          a.stream, a, parts);
@@ -441,7 +493,7 @@ hipError_t head_backward(const HeadArgs& a) {
     head_dispatch(a, [&](auto t, auto vec, auto lg, auto c) {
       constexpr int LG = decltype(lg)::value;
       const int heads = a.q_heads > a.k_heads ? a.q_heads : a.k_heads;
-      const int parts = head_parts(a.tokens, heads, 64 / LG, 4096);
+      const int parts = head_parts(a.tokens, ceil_div(heads, 64 / LG), 4096);
       const long long jobs = (long long)a.tokens * parts;
       blocks = (int)(jobs < 256 * 16 ? (jobs + 15) / 16 : 256);
       hipLaunchKernelGGL((head_bwd_kernel<decltype(t), decltype(vec)::value, LG, decltype(c)::value>), dim3(blocks),

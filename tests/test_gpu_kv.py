@@ -180,3 +180,49 @@ def test_captured_and_replayed():
             torch.cuda.synchronize()
             for got, x in zip(out, (k, v)):
                 assert np.array_equal(got.double().cpu().numpy(), O.held(x.float().cpu().numpy(), kind))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prompts(kind, dtype):
+    """Enough tokens that values go four at a time: slots in runs that begin and end
+    anywhere, some left out, the last group of four not full."""
+    rng = np.random.default_rng(14)
+    H, D, page, T = 128, 64, 16, 131
+    cache = nq.KvCache(40, H, D, page=page, kind=kind, device=DEV)
+    everywhere = torch.arange(40 * page, device=DEV)
+    k, v = (tokens(rng, 40 * page, H, D, dtype) for _ in range(2))
+    nq.kv_write(k.to(DEV), v.to(DEV), cache, everywhere)
+    check(cache, everywhere, k, v)
+    runs = [np.arange(4, 45), np.arange(61, 64), np.arange(100, 120), [-1, 300], np.arange(202, 250), np.arange(400, 440)]
+    slots = torch.from_numpy(np.concatenate(runs)[:T])
+    nk, nv = (tokens(rng, T, H, D, dtype) for _ in range(2))
+    nq.kv_write(nk.to(DEV), nv.to(DEV), cache, slots.to(DEV))
+    on = slots >= 0
+    k[slots[on]], v[slots[on]] = nk[on], nv[on]
+    check(cache, everywhere, k, v)
+    for got, x in zip(read(cache, slots.to(DEV)), (k, v)):
+        assert np.array_equal(got[on.numpy()], O.held(x[slots[on]].float().numpy(), kind)) and not got[~on.numpy()].any()
+
+
+@pytest.mark.parametrize("kind", ["int8", "int4"])
+def test_codes_beside_ties(kind):
+    """Values on the ties between two codes and next to them on both sides, over scales
+    of every size."""
+    most = O.MOST[kind]
+    D = 256
+    group = D if kind == "int8" else 32
+    rows = []
+    for e in list(range(-126, 121, 13)) + [-130, -133, -99, -100, -101, 99, 100, 101]:
+        for scale in (1.0, 1.9921875, 1.3671875):
+            s = np.float32(scale) * np.float32(2.0) ** np.float32(e)
+            tie = (np.arange(D) % (2 * most) - most + 0.5).astype(np.float32) * s
+            for off in (-1, 0, 1):
+                x = (tie.view(np.int32) + off).view(np.float32).copy()
+                x[::group] = most * s
+                rows.append(x)
+    x = torch.from_numpy(np.stack(rows)[:, None])
+    cache = nq.KvCache(-(-len(rows) // 16), 1, D, page=16, kind=kind, device=DEV)
+    slots = torch.arange(len(rows), device=DEV)
+    nq.kv_write(x.to(DEV), x.flip(0).to(DEV), cache, slots)
+    check(cache, slots, x, x.flip(0))
