@@ -16,7 +16,7 @@
 // whose scale multiplies the product of keys and queries in fp32 and, for values, the
 // weight.  4-bit codes enter as c + 24 (set into the mantissa of 16) and 24 times
 // the sum of what they are multiplied with is taken off by the same MFMA.  Scores, maximum, sum and
-// output are fp32.  Weights are rounded to bf16 (2^-9 each, and the sum of bf16 values
+// output are fp32.  Weights are rounded to bf16 (2^-8 each, and the sum of bf16 values
 // is taken over the rounded ones, so that a token that outweighs the others is exact);
 // FINE, for fp32 queries or outputs, takes weights and queries as three bf16 pieces,
 // exactly, and 4-bit codes as c, for 24 times the sum of the weights would cost some of
@@ -701,7 +701,12 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int hb, int 
 template <int D, int KIND, bool FINE>
 void attn_launch(const AttnArgs& a) {
   const int heads = a.cache.heads, units = heads * head_tiles(a.q_heads / heads);
-  if (a.max_length <= 512) {
+  // Units as they are, a workgroup each, where none is long, or there are many and none very
+  // long: no join (some 6 us with its launch), but a long unit beside short ones is one
+  // workgroup's.  8 key heads of 128, 8 bits, one launch and two: 16 x 1024 tokens 13.8 and 18.2
+  // us, 64 x 2048 48.2 and 54.7, 16 x 2048 23.0 and 23.3, 1 x 1024 12.1 and 10.7, 1 x 2048 20.0 and 11.4.
+  const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
+  if (longest <= 1024 || (longest <= 2048 && (long long)a.B * units >= ATTN_GRID)) {
     hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, false>), dim3((unsigned)(a.B * units)), dim3(64 * ATTN_WAVES), 0, a.stream, a);
     return;
   }

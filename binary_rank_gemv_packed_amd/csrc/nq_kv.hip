@@ -1,7 +1,7 @@
 // The paged cache of keys and values: writing tokens to their slots and reading
 // slots back.  A held value is bf16(x), or s c with c = x / s to the nearest whole
 // number and s = bf16(max |x| / 127) over a head's channels (8 bits) or bf16(max |x| / 7)
-// over 32 of them (4 bits): off by at most half of s, s within 2^-9 of the quotient.
+// over 32 of them (4 bits): off by at most half of s, s within 2^-8 of the quotient.
 // Both kernels are bound by memory.
 #include "nq_kv.h"
 #include "nq_internal.h"

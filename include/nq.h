@@ -441,11 +441,12 @@ nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots,
  *             outside the cache, where one is, makes outputs of its sequence NaN and is not read
  *   workspace : device, >= nq_kv_attention_workspace_bytes(C), 256-byte aligned; no initial contents
  * Scores, softmax statistics and sums are fp32; weights of the softmax are rounded to
- * bf16 (2^-9) for bf16 q and y, else not.  What lies in slots that are not seen
+ * bf16 (2^-8) for bf16 q and y, else not.  What lies in slots that are not seen
  * does not matter.  Asynchronous on `stream`, capturable (lengths and table are read by
  * the kernels); calls that overlap in time need workspaces of their own; repeated calls
- * give identical bits.  B == 0 launches nothing.  max_length chooses between one launch
- * (up to 512) and a split over the length with a join. */
+ * give identical bits.  B == 0 launches nothing.  max_length and the window choose
+ * between one launch (up to 1024 tokens, 2048 for large batches) and a split over the
+ * length with a join. */
 size_t nq_kv_attention_workspace_bytes(const nq_kv_cache* C);
 nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_t q_dtype, int32_t q_heads,
                           const int32_t* table, int32_t table_width, const int32_t* lengths, int32_t max_length,

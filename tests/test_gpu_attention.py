@@ -4,7 +4,8 @@ Tolerances (derived, not fitted), with e = 2^-24, P = the softmax's weights and
 M = sum P |v|.  A score is a sum of D products (of 24 + |c| instead of |c| for 4 bits)
 held in fp32: off by under (D + 8) e of the sum of their magnitudes, at most d; a weight
 by twice that and 2^-22 for its exponential, and so are the weights' sum and the quotient.
-A weight is rounded to bf16 (2^-9), or for fp32 q or y taken as three, off by 2^-23 at most.  The
+A weight is rounded to bf16, which has 8 significant bits: half a step of 1.0 is 2^-8, and of no value
+more; or for fp32 q or y taken as three, off by 2^-23 at most.  The
 sum over n tokens is at most n / 32 + 64 sums.  Altogether (2 (2 d + 2^-22) +
 w + (n / 32 + 64) e) (M + 24 s for 4 bits), and half a step of the output's type."""
 import numpy as np
@@ -74,7 +75,7 @@ class Case:
                 sk = float(O.scales(self.k[b], "int4").max())
                 big = big + abs(scale) * 24 * sk * np.abs(self.q[b].double().numpy()).sum(1, keepdims=True)
             d = (self.D + 8) * E * big
-            w = 2.0 ** -23 if fine else 2.0 ** -9
+            w = 2.0 ** -23 if fine else 2.0 ** -8
             n = self.lengths[b]
             tol = (2 * (2 * d + 2.0 ** -22) + w + (n / 32 + 64) * E) * mag
             tol = tol + torch.finfo(self.y).eps / 2 * (np.abs(want) + tol) + 1e-42
@@ -89,10 +90,10 @@ LENGTHS = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 100, 127, 128, 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("q,y", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
 def test_lengths(D, kind, q, y):
-    """One launch (up to 512 tokens), and the same lengths beside a longer one."""
+    """One launch (short sequences), and the same lengths beside a longer one."""
     c = Case(LENGTHS, 8, 2, D, 64, kind, q, y)
     c.check(c.run(max_length=512))
-    c = Case(LENGTHS + [1100], 8, 2, D, 64, kind, q, y, seed=1)
+    c = Case(LENGTHS + [2100], 8, 2, D, 64, kind, q, y, seed=1)
     c.check(c.run())
 
 
@@ -100,33 +101,35 @@ def test_lengths(D, kind, q, y):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("long", [False, True])
 def test_heads(Hq, H, kind, long):
-    c = Case([70, 0, 333, 1500 if long else 12], Hq, H, 64, 32, kind, BF, F32)
+    c = Case([70, 0, 333, 2500 if long else 12], Hq, H, 64, 32, kind, BF, F32)
     c.check(c.run())
 
 
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 1024])
 @pytest.mark.parametrize("kind", KINDS)
 def test_pages(page, kind):
-    for lengths in ([5, 16, 200, 33], [5, 1040, 777, 16]):
+    for lengths in ([5, 16, 200, 33], [5, 2200, 777, 16]):
         c = Case(lengths, 4, 2, 96, page, kind, F32)
         c.check(c.run())
 
 
-@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 31, 32, 33, 100, 600, 5000])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 31, 32, 33, 100, 1100, 5000])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("page", [16, 64])
 def test_windows(window, kind, page):
-    for lengths in ([1, 16, 17, 48, 65, 0, 300], [40, 2000, 1, 1311, 64]):
+    for lengths in ([1, 16, 17, 48, 65, 0, 300], [40, 2500, 1, 1311, 64]):
         c = Case(lengths, 8, 2, 64, page, kind, BF, F32, window=window)
         c.check(c.run())
 
 
-@pytest.mark.parametrize("lengths", [[40000], [3, 30000, 1, 1, 9000], [1] * 700, [129] * 300, list(range(0, 1200, 7))])
+@pytest.mark.parametrize("lengths", [[40000], [3, 30000, 1, 1, 9000], [1] * 700, [129] * 300, list(range(0, 1200, 7)), list(range(0, 2200, 13))])
 @pytest.mark.parametrize("kind,D", [("bf16", 128), ("int8", 128), ("int4", 64)])
 def test_shares(lengths, kind, D):
     """One long sequence, a few of very different lengths, many of one token: every way
     that units fall into the workgroups' shares."""
     c = Case(lengths, 4, 2, D, 16, kind, BF, F32)
+    if max(lengths) <= 2048:  # a wide table: the host does not know that they are short
+        c.gt = torch.cat([c.gt, torch.full((len(lengths), 300), -1, dtype=torch.int32, device=DEV)], dim=1)
     rows = None if len(lengths) < 100 else list(range(0, len(lengths), 17)) + [len(lengths) - 1]
     c.check(c.run(), rows)
 
@@ -137,9 +140,9 @@ def test_loud_scores(kind, long):
     """Scores far apart (one token outweighs the others), falling and rising along the
     sequence, and of one size."""
     for loud in (0.0, 30.0, 1000.0):
-        c = Case([400, 37, 1200 if long else 60], 8, 2, 128, 64, kind, F32, loud=loud)
+        c = Case([400, 37, 2200 if long else 60], 8, 2, 128, 64, kind, F32, loud=loud)
         c.check(c.run())
-    c = Case([500, 1400 if long else 250], 2, 1, 64, 16, "bf16", F32)
+    c = Case([500, 2400 if long else 250], 2, 1, 64, 16, "bf16", F32)
     for b, up in ((0, 1.0), (1, -1.0)):  # keys that grow along q
         n = c.lengths[b]
         c.k[b][:] = (c.q[b, :1].numpy()[None] * (np.linspace(-3, 3, n) * up)[:, None, None]).astype(np.float32)
@@ -157,7 +160,7 @@ def test_scale():
 @pytest.mark.parametrize("kind", KINDS)
 def test_what_is_not_seen_does_not_matter(kind):
     """NaN, infinities and any codes in unseen slots, pages and rows: the same bits."""
-    for lengths, window in (([1, 17, 100, 250], 0), ([70, 1000, 31], 40)):
+    for lengths, window in (([1, 17, 100, 250], 0), ([70, 1000, 31], 40), ([70, 2500, 31], 2100)):
         outs = []
         for fill in (0x00, 0xFF, 0x7F, 0x80):
             c = Case(lengths, 8, 2, 128, 32, kind, BF, F32, window=window)
@@ -175,7 +178,7 @@ def test_values_that_are_not_finite(long):
     """As the formula: a NaN key makes its heads NaN, a NaN or infinite value its channel; other
     heads and sequences keep their bits.  8 bits: the whole head; 4 bits: its 32 channels."""
     for kind in KINDS:
-        c = Case([60, 61, 1000 if long else 62], 4, 2, 64, 16, kind, BF, F32)
+        c = Case([60, 61, 2200 if long else 62], 4, 2, 64, 16, kind, BF, F32)
         clean = c.run()
         first = torch.from_numpy(c.slots[:1]).to(DEV)
         k, v = torch.from_numpy(c.k[0][:1]).to(DEV), torch.from_numpy(c.v[0][:1]).to(DEV)
@@ -193,7 +196,7 @@ def test_values_that_are_not_finite(long):
 def test_queries_that_are_not_finite_stay_in_their_head():
     for q in (BF, F32):
         for long in (False, True):
-            c = Case([50, 900 if long else 70], 8, 2, 64, 16, "int4", q)
+            c = Case([50, 2300 if long else 70], 8, 2, 64, 16, "int4", q)
             clean = c.run()
             c.gq[0, 3, 7], c.gq[1, 6, 0] = float("nan"), float("inf")
             y = c.run()
@@ -207,7 +210,7 @@ def test_queries_that_are_not_finite_stay_in_their_head():
 def test_bad_lengths_and_pages_make_their_sequence_nan(kind, long):
     """Lengths below zero or above what the table or max_length allow, pages outside the
     cache: NaN for that sequence, its neighbours keep their bits."""
-    n = 1500 if long else 130
+    n = 2500 if long else 130
     c = Case([n, 100, 64, 33, 90, 20], 4, 2, 64, 16, kind, BF, F32)
     want = c.run()
     bad = c.gl.clone()
@@ -239,7 +242,7 @@ def test_repeated_and_reordered_batches():
 def test_captured_and_replayed_while_sequences_grow(kind):
     """One captured call over lengths and a table that change between the replays, on a
     workspace that eager calls use in between."""
-    c = Case([700, 40, 0, 1300], 8, 2, 128, 16, kind, BF)
+    c = Case([700, 40, 0, 2300], 8, 2, 128, 16, kind, BF)
     ws = nq.new_kv_workspace(4, 8, c.cache)
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
@@ -248,7 +251,7 @@ def test_captured_and_replayed_while_sequences_grow(kind):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         y = c.run(workspace=ws)
-    for lengths in ([700, 40, 0, 1300], [1, 17, 0, 600], [640, 0, 0, 1], [0, 0, 0, 0], [699, 33, 0, 1299]):
+    for lengths in ([700, 40, 0, 2300], [1, 17, 0, 600], [640, 0, 0, 1], [0, 0, 0, 0], [699, 33, 0, 1299]):
         c.gl.copy_(torch.tensor(lengths, dtype=torch.int32))
         c.gq.copy_(torch.randn(c.gq.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(sum(lengths))))
         want = c.run(workspace=ws)
