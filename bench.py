@@ -28,6 +28,8 @@ chain with the norms between its blocks, on 4-bit and on binary linears) and
   python bench.py --suite 7b --out FILE            7B shapes, B in {1,2,4,8,16}, 0.55/0.8/1.0 bpw:
                                                    per-shape GB/s over >= 1 GiB of rotating layer copies
   python bench.py --initializer-only | --variants-only | --int4-only
+  python bench.py --attention-only                 what stands between q/k/v and o in those blocks: heads'
+                                                   norms and rotation, cache write, attention over the cache
 """
 from __future__ import annotations
 
@@ -70,6 +72,7 @@ def parse():
     ap.add_argument("--initializer-only", action="store_true", help="run only the ADMM initialiser section")
     ap.add_argument("--no-int4", action="store_true", help="skip the 4-bit chain section")
     ap.add_argument("--int4-only", action="store_true", help="run only the 4-bit chain section")
+    ap.add_argument("--attention-only", action="store_true", help="run only the attention section")
     ap.add_argument("--prefill-only", action="store_true", help="run only the 2048-token prefill section")
     ap.add_argument("--suite", default=None, choices=["7b"])
     ap.add_argument("--out", default=None)
@@ -795,6 +798,56 @@ def run_int4(dev, distinct=8, nblocks=80, bpw=0.8, group=128):
     return out
 
 
+def run_attention(dev, distinct=4, nblocks=80):
+    """One token of each of B sequences through what stands between the q/k/v and o
+    linears of 70B-shaped blocks (64 query heads, 8 key heads of 128): norm and
+    rotation of the heads with the new token written to the cache, and its attention over
+    `context` tokens, the cache in bf16, 8 and 4 bits.  `distinct` caches take turns;
+    one HIP graph of `nblocks` blocks.  GB/s counts the cache's codes and scales."""
+    import torch
+    import binary_rank_gemv_packed_amd as nq
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(20260208)
+    rand = lambda *shape: torch.randn(*shape, generator=gen, device=dev).to(torch.bfloat16)  # noqa: E731
+    D, Hq, Hk, page = 128, 64, 8, 64
+    norm = nq.HeadNorm(D, w_q=1 + 0.1 * rand(D), w_k=1 + 0.1 * rand(D),
+                       inv_freq=500000.0 ** (-torch.arange(0, D, 2, device=dev, dtype=torch.float64) / D))
+    stream = torch.cuda.Stream()
+    out = {"workload": f"{nblocks} blocks, {Hq} query heads, {Hk} key heads of {D}, bf16", "cases": []}
+    for B, context in ((1, 4096), (1, 32768), (32, 4096)):
+        for kind in ("bf16", "int8", "int4"):
+            pages = -(-context // page)
+            lengths = torch.full((B,), context, dtype=torch.int32, device=dev)
+            caches = []
+            for _ in range(distinct):
+                cache = nq.KvCache(B * pages, Hk, D, page=page, kind=kind, device=dev)
+                table = torch.randperm(B * pages, generator=gen, device=dev).int().view(B, pages)
+                for lo in range(0, B * pages * page, 1 << 16):
+                    n = min(1 << 16, B * pages * page - lo)
+                    nq.kv_write(rand(n, Hk, D), rand(n, Hk, D), cache, torch.arange(lo, lo + n, device=dev))
+                slots = table.long()[:, (context - 1) // page] * page + (context - 1) % page
+                caches.append((cache, table, slots))
+            q, k, v, ws = rand(B, Hq, D), rand(B, Hk, D), rand(B, Hk, D), nq.new_kv_workspace(B, Hq, caches[0][0])
+            at = (lengths - 1).long()
+
+            def step():
+                for b in range(nblocks):
+                    cache, table, slots = caches[b % distinct]
+                    q2 = nq.head_norm_write(q, k, v, at, norm, cache, slots)
+                    y = nq.kv_attention(q2, cache, table, lengths, workspace=ws)
+                return y
+
+            ms, _ = time_graph(torch, stream, step, 3, 10)
+            held = B * context * caches[0][0].page_bytes / page
+            out["cases"].append({"batch": B, "context": context, "cache": kind, "ms_per_step": round(ms, 4),
+                                 "us_per_block": round(ms * 1e3 / nblocks, 2),
+                                 "gbs": round(held * nblocks / (ms * 1e-3) / 1e9, 1)})
+            log(f"[bench] attention {B} x {context} {kind}: {ms:.3f} ms per step, {out['cases'][-1]['gbs']} GB/s of cache")
+            del caches
+    torch.cuda.empty_cache()
+    return out
+
+
 # ------------------------------------------------------------------ 7B per-shape suite
 def run_suite7b(args):
     import torch
@@ -1039,6 +1092,8 @@ def main():
         print(json.dumps({"initializer": run_initializer("cuda:0")}), flush=True)
     elif args.variants_only:
         print(json.dumps({"variants": run_variants("cuda:0")}), flush=True)
+    elif args.attention_only:
+        print(json.dumps({"attention": run_attention("cuda:0")}), flush=True)
     elif args.int4_only:
         print(json.dumps({"int4": run_int4("cuda:0")}), flush=True)
     elif args.prefill_only:

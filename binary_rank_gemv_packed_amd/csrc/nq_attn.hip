@@ -35,6 +35,8 @@ typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x3 __attribute__((ext_vector_type(3), aligned(4)));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int ATTN_WAVES = 4;
 constexpr int ATTN_GRID = 512;    // workgroups that share the tokens of all sequences
@@ -162,106 +164,140 @@ __device__ __forceinline__ void lane_bytes(const uint8_t* tile, int lane, uint32
   }
 }
 
-template <int D, int KIND>
-struct Pair {
-  static constexpr int LB = kv_lane_bytes(KIND, D), NG = kv_groups(KIND, D), SW = NG ? 4 * NG : 1;
-  uint32_t k[2][LB / 4], v[2][LB / 4];
-  uint32_t s[2][SW];  // scales of the lane's four slots: keys [NG], values [NG], two words each
-  // (lane: where no pair is left every lane reads lane 0's part, a line of each piece)
-  __device__ __forceinline__ void load(int i, const uint8_t* tile, const uint8_t* scales, int lane) {
-    lane_bytes<LB>(tile, lane, k[i]);
-    lane_bytes<LB>(tile + kv_half_bytes(KIND, D), lane, v[i]);
-    if constexpr (NG > 0) {
+// Where the two tiles of a pair lie (the same for the wave).
+struct Where {
+  const uint8_t* tile[2];
+  const uint8_t* scales[2];
+};
+
+// A pair's keys or values, and the scales of the lane's four slots of either tile,
+// NG groups, two words each.
+template <int D, int KIND, bool VALUE>
+struct Half {
+  static constexpr int LB = kv_lane_bytes(KIND, D), NG = kv_groups(KIND, D);
+  uint32_t w[2][LB / 4], s[2][NG ? 2 * NG : 1];
+  // lane: where no pair is left every lane reads lane 0's part, a line of each piece
+  __device__ __forceinline__ void load(const Where& at, int lane) {
 #pragma unroll
-      for (int p = 0; p < NG; p++) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(scales + (lane >> 4) * 16 * NG + 16 * p);
+    for (int i = 0; i < 2; i++) {
+      lane_bytes<LB>(at.tile[i] + (VALUE ? kv_half_bytes(KIND, D) : 0), lane, w[i]);
+      const uint8_t* q = at.scales[i] + (lane >> 4) * 16 * NG + (VALUE ? 8 * NG : 0);
+#pragma unroll
+      for (int p = 0; p < NG / 2; p++) {
+        const u32x4 u = *reinterpret_cast<const u32x4_at4*>(q + 16 * p);
 #pragma unroll
         for (int e = 0; e < 4; e++) s[i][4 * p + e] = u[e];
       }
+      if constexpr (NG % 2) {
+        const u32x2 u = *reinterpret_cast<const u32x2*>(q + 8 * (NG - 1));
+        s[i][2 * NG - 2] = u[0];
+        s[i][2 * NG - 1] = u[1];
+      }
     }
   }
-  __device__ __forceinline__ float scale(int i, int value, int group, int j) const {
-    const uint32_t w = s[i][(value * NG + group) * 2 + j / 2];
-    return j & 1 ? high_f32(w) : low_f32(w);
+  __device__ __forceinline__ float scale(int i, int group, int j) const {
+    const uint32_t u = s[i][group * 2 + j / 2];
+    return j & 1 ? high_f32(u) : low_f32(u);
   }
-  // operand of 32 channels of 16 keys
+  // keys: operand of 32 channels of 16 slots
   template <bool FINE>
   __device__ __forceinline__ u32x4 keys(int i, int c, const Nibbles& nb) const {
     if constexpr (KIND == KV_BF16) {
-      return u32x4{k[i][4 * c], k[i][4 * c + 1], k[i][4 * c + 2], k[i][4 * c + 3]};
+      return u32x4{w[i][4 * c], w[i][4 * c + 1], w[i][4 * c + 2], w[i][4 * c + 3]};
     } else if constexpr (KIND == KV_INT8) {
-      const u32x2 a = bytes_bf16(k[i][2 * c]), b = bytes_bf16(k[i][2 * c + 1]);
+      const u32x2 a = bytes_bf16(w[i][2 * c]), b = bytes_bf16(w[i][2 * c + 1]);
       return u32x4{a[0], a[1], b[0], b[1]};
     } else {
-      const uint32_t w = k[i][c];
-      if constexpr (FINE) return u32x4{codes_bf16(w, 0), codes_bf16(w, 1), codes_bf16(w, 2), codes_bf16(w, 3)};
-      return u32x4{nb.bf16(w, 0), nb.bf16(w, 1), nb.bf16(w, 2), nb.bf16(w, 3)};
+      const uint32_t u = w[i][c];
+      if constexpr (FINE) return u32x4{codes_bf16(u, 0), codes_bf16(u, 1), codes_bf16(u, 2), codes_bf16(u, 3)};
+      return u32x4{nb.bf16(u, 0), nb.bf16(u, 1), nb.bf16(u, 2), nb.bf16(u, 3)};
     }
   }
-  // operand of 16 channels of the pair's values; keep: the bits of bf16 values that are seen
+  // values: operand of 16 channels of the pair; keep: the bits of bf16 values that are seen
   template <bool FINE>
   __device__ __forceinline__ u32x4 values(int x, const uint32_t (&keep)[4], const Nibbles& nb) const {
     if constexpr (KIND == KV_BF16) {
-      return u32x4{v[0][2 * x] & keep[0], v[0][2 * x + 1] & keep[1], v[1][2 * x] & keep[2], v[1][2 * x + 1] & keep[3]};
+      return u32x4{w[0][2 * x] & keep[0], w[0][2 * x + 1] & keep[1], w[1][2 * x] & keep[2], w[1][2 * x + 1] & keep[3]};
     } else if constexpr (KIND == KV_INT8) {
-      const u32x2 a = bytes_bf16(v[0][x]), b = bytes_bf16(v[1][x]);
+      const u32x2 a = bytes_bf16(w[0][x]), b = bytes_bf16(w[1][x]);
       return u32x4{a[0], a[1], b[0], b[1]};
     } else {
       const int h = x & 1;
-      const uint32_t a = v[0][x / 2], b = v[1][x / 2];
+      const uint32_t a = w[0][x / 2], b = w[1][x / 2];
       if constexpr (FINE) return u32x4{codes_bf16(a, h), codes_bf16(a, 2 + h), codes_bf16(b, h), codes_bf16(b, 2 + h)};
       return u32x4{nb.bf16(a, h), nb.bf16(a, 2 + h), nb.bf16(b, h), nb.bf16(b, 2 + h)};
     }
   }
 };
 
+// Queries as the operand of the MFMA, in shared memory: [piece][32 channels][64 lanes],
+// lane L channels 8 (L >> 4) .. + 7 of head L & 15.  FINE: three pieces.
+constexpr int query_pieces(bool fine) { return fine ? 3 : 1; }
+
+// A wave's share of them: channels 32 c .. for c = wave, wave + 4.
+template <int D, bool FINE>
+struct Queries {
+  static constexpr int CH = D / 32, EACH = (CH + ATTN_WAVES - 1) / ATTN_WAVES, PIECES = query_pieces(FINE);
+  u32x4_at2 raw[EACH][FINE ? 2 : 1];
+  // row: the lane's head, null for none
+  __device__ __forceinline__ void load(const void* row, int dtype, int wave, int lane) {
+#pragma unroll
+    for (int j = 0; j < EACH; j++) {
+      const int at = 32 * (wave + ATTN_WAVES * j) + 8 * (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < (FINE ? 2 : 1); i++) raw[j][i] = u32x4_at2{0u, 0u, 0u, 0u};
+      if (!row || at >= D) continue;
+      if (FINE && dtype == 0) {
+#pragma unroll
+        for (int i = 0; i < (FINE ? 2 : 1); i++) raw[j][i] = reinterpret_cast<const u32x4_at2*>(static_cast<const float*>(row) + at)[i];
+      } else {
+        raw[j][0] = *reinterpret_cast<const u32x4_at2*>(static_cast<const uint16_t*>(row) + at);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(uint32_t (*to)[64][4], int dtype, int wave, int lane) const {
+#pragma unroll
+    for (int j = 0; j < EACH; j++) {
+      const int c = wave + ATTN_WAVES * j;
+      if (c >= CH) continue;
+      u32x4 out[PIECES];
+#pragma unroll
+      for (int p = 0; p < PIECES; p++) out[p] = u32x4{0u, 0u, 0u, 0u};
+      if (FINE && dtype == 0) {  // pieces cut off, not rounded: none passes the largest value
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          float v[2] = {__uint_as_float(raw[j][FINE ? i / 2 : 0][2 * i % 4]), __uint_as_float(raw[j][FINE ? i / 2 : 0][2 * i % 4 + 1])};
+          uint32_t part[2];
+          const bool finite[2] = {fabsf(v[0]) <= 3.402823466e38f, fabsf(v[1]) <= 3.402823466e38f};
+#pragma unroll
+          for (int p = 0; p < PIECES; p++) {
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              part[h] = __float_as_uint(v[h]) & 0xffff0000u;
+              // an infinity or a NaN (a quiet one) is one piece
+              if (!finite[h]) part[h] = p ? 0u : v[h] != v[h] ? 0x7fc00000u : part[h];
+              v[h] -= __uint_as_float(part[h]);
+            }
+            out[p][i] = high_halves(part[1], part[0]);
+          }
+        }
+      } else {
+        out[0] = raw[j][0];
+      }
+#pragma unroll
+      for (int p = 0; p < PIECES; p++) *reinterpret_cast<u32x4*>(to[p * CH + c][lane]) = out[p];
+    }
+  }
+};
+
 template <int D, int KIND, bool FINE>
 struct Wave {
-  static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = FINE ? 3 : 1;
-  u32x4 q[PIECES][CH];
-  static constexpr bool BIAS = KIND == KV_INT4 && !FINE;
-  v4f less[BIAS ? CH : 1];  // -24 times the sum of the queries' 32 channels
+  static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE);
+  static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24
   v4f o[XT];
   float m, safe, l;
   int lane;
   Nibbles nb;
-
-  // queries of the lane's head (row null: zeros), eight channels of each 32
-  __device__ __forceinline__ void queries(const void* row, int dtype) {
-#pragma unroll
-    for (int c = 0; c < CH; c++) {
-#pragma unroll
-      for (int p = 0; p < PIECES; p++) q[p][c] = u32x4{0u, 0u, 0u, 0u};
-      if (!row) continue;
-      const int at = 32 * c + 8 * (lane >> 4);
-      if (dtype == 2) {
-        const uint16_t* r = static_cast<const uint16_t*>(row) + at;
-#pragma unroll
-        for (int i = 0; i < 4; i++) q[0][c][i] = r[2 * i] | (uint32_t)r[2 * i + 1] << 16;
-      } else if constexpr (FINE) {  // pieces cut off, not rounded: none passes the largest value
-        const float* r = static_cast<const float*>(row) + at;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          float a = r[2 * i], b = r[2 * i + 1];
-          const bool fine_a = fabsf(a) <= 3.402823466e38f, fine_b = fabsf(b) <= 3.402823466e38f;
-#pragma unroll
-          for (int p = 0; p < 3; p++) {
-            // of an infinity or a NaN only one piece, a quiet one
-            const float ha = fine_a ? __uint_as_float(__float_as_uint(a) & 0xffff0000u) : p ? 0.0f : a != a ? __uint_as_float(0x7fc00000u) : a;
-            const float hb = fine_b ? __uint_as_float(__float_as_uint(b) & 0xffff0000u) : p ? 0.0f : b != b ? __uint_as_float(0x7fc00000u) : b;
-            q[p][c][i] = high_halves(__float_as_uint(hb), __float_as_uint(ha));
-            a -= ha;
-            b -= hb;
-          }
-        }
-      }
-    }
-    if constexpr (BIAS) {
-      const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
-#pragma unroll
-      for (int c = 0; c < CH; c++) less[c] = mfma(minus, q[0][c], v4f{0.0f, 0.0f, 0.0f, 0.0f});
-    }
-  }
 
   __device__ __forceinline__ void begin() {
     m = NEG_INF;
@@ -270,42 +306,46 @@ struct Wave {
     for (int x = 0; x < XT; x++) o[x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // 32 tokens from `first` on, of which those from lo to n - 1 are seen
-  __device__ __forceinline__ void step(Pair<D, KIND>& t, float c, int first, int lo, int n) {
-    const bool edge = first < lo || first + ATTN_PAIR > n;
-    float x[8];
+  // the scores (in powers of two) of the lane's 2 x 4 tokens of its head
+  __device__ __forceinline__ void scores(const Half<D, KIND, false>& t, const uint32_t (*q)[64][4], float c, float (&x)[8]) const {
+    const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
+    v4f s[2];
+    s[0] = s[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      v4f s = {0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (KIND == KV_INT4) {
+    for (int ch = 0; ch < CH; ch++) {
+      u32x4 query[PIECES];
 #pragma unroll
-        for (int ch = 0; ch < CH; ch++) {
-          v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (BIAS) d = less[ch];
-          const u32x4 key = t.template keys<FINE>(i, ch, nb);
+      for (int p = 0; p < PIECES; p++) query[p] = *reinterpret_cast<const u32x4*>(q[p * CH + ch][lane]);
+      v4f less = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (BIAS) less = mfma(minus, query[0], less);
 #pragma unroll
-          for (int p = PIECES - 1; p >= 0; p--) d = mfma(key, q[p][ch], d);
+      for (int i = 0; i < 2; i++) {
+        const u32x4 key = t.template keys<FINE>(i, ch, nb);
+        v4f d = KIND == KV_INT4 ? less : s[i];
 #pragma unroll
-          for (int j = 0; j < 4; j++) s[j] = fmaf(t.scale(i, 0, ch, j), d[j], s[j]);
-        }
-      } else {
+        for (int p = PIECES - 1; p >= 0; p--) d = mfma(key, query[p], d);
+        if constexpr (KIND == KV_INT4) {
 #pragma unroll
-        for (int ch = 0; ch < CH; ch++) {
-          const u32x4 key = t.template keys<FINE>(i, ch, nb);
-#pragma unroll
-          for (int p = PIECES - 1; p >= 0; p--) s = mfma(key, q[p][ch], s);
-        }
-        if constexpr (KIND == KV_INT8) {
-#pragma unroll
-          for (int j = 0; j < 4; j++) s[j] *= t.scale(i, 0, 0, j);
+          for (int j = 0; j < 4; j++) s[i][j] = fmaf(t.scale(i, ch, j), d[j], s[i][j]);
+        } else {
+          s[i] = d;
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; j++) x[4 * i + j] = s[j] * c;
     }
-    // what lies in slots that are not seen may be anything: their values (scales) become zero
-    uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-    if (edge) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      if constexpr (KIND == KV_INT8) x[j] = s[j / 4][j & 3] * (c * t.scale(j / 4, 0, j & 3));
+      else x[j] = s[j / 4][j & 3] * c;
+    }
+  }
+
+  // Scores to weights.  32 tokens from `first` on, of which those from lo to n - 1 are seen:
+  // the others weigh nothing and `keep` masks their values (bf16) or scales, for what
+  // lies there may be anything.
+  __device__ __forceinline__ void weigh(float (&x)[8], int first, int lo, int n, uint32_t (&keep)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) keep[i] = ~0u;
+    if (first < lo || first + ATTN_PAIR > n) {
       asm volatile("");  // a branch: made into selects this costs 45 instructions a step
 #pragma unroll
       for (int j = 0; j < 8; j++) {
@@ -315,49 +355,52 @@ struct Wave {
           keep[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
         }
       }
-      if constexpr (KIND != KV_BF16) {
-#pragma unroll
-        for (int g = 0; g < NG; g++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) t.s[i / 2][2 * (NG + g) + i % 2] &= keep[i];
-      }
     }
     float top = NEG_INF;
 #pragma unroll
     for (int j = 0; j < 8; j++) top = fmaxf(top, x[j]);
     if (__any(top > m + ATTN_RISE)) raise(top);
-    float p[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) p[j] = __builtin_amdgcn_exp2f(x[j] - safe);
+    for (int j = 0; j < 8; j++) x[j] = __builtin_amdgcn_exp2f(x[j] - safe);
+  }
+
+  __device__ __forceinline__ void add(Half<D, KIND, true>& t, const float (&p)[8], const uint32_t (&keep)[4], bool edge) {
     if constexpr (NG == 0) {
       u32x4 w[PIECES];
       weights(p, w);
 #pragma unroll
       for (int j = 0; j < 4; j++) l += FINE ? p[2 * j] + p[2 * j + 1] : low_f32(w[0][j]) + high_f32(w[0][j]);
 #pragma unroll
-      for (int xt = 0; xt < XT; xt++) {
-        const u32x4 value = t.template values<FINE>(xt, keep, nb);
+      for (int x = 0; x < XT; x++) {
+        const u32x4 value = t.template values<FINE>(x, keep, nb);
 #pragma unroll
-        for (int i = PIECES - 1; i >= 0; i--) o[xt] = mfma(value, w[i], o[xt]);
+        for (int i = PIECES - 1; i >= 0; i--) o[x] = mfma(value, w[i], o[x]);
       }
     } else {
+      if (edge) {
+        asm volatile("");
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int k = 0; k < 2 * NG; k++) t.s[i][k] &= keep[2 * i + (k & 1)];
+      }
 #pragma unroll
       for (int j = 0; j < 8; j++) l += p[j];
 #pragma unroll
       for (int g = 0; g < NG; g++) {
         float ps[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) ps[j] = p[j] * t.scale(j / 4, 1, g, j & 3);
+        for (int j = 0; j < 8; j++) ps[j] = p[j] * t.scale(j / 4, g, j & 3);
         u32x4 w[PIECES];
         weights(ps, w);
 #pragma unroll
-        for (int xt = g * XT / NG; xt < (g + 1) * XT / NG; xt++) {
-          const u32x4 value = t.template values<FINE>(xt, keep, nb);
+        for (int x = g * XT / NG; x < (g + 1) * XT / NG; x++) {
+          const u32x4 value = t.template values<FINE>(x, keep, nb);
 #pragma unroll
-          for (int i = PIECES - 1; i >= 0; i--) o[xt] = mfma(value, w[i], o[xt]);
+          for (int i = PIECES - 1; i >= 0; i--) o[x] = mfma(value, w[i], o[x]);
           if constexpr (BIAS) {
             const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
-            o[xt] = mfma(minus, w[0], o[xt]);
+            o[x] = mfma(minus, w[0], o[x]);
           }
         }
       }
@@ -444,12 +487,14 @@ struct Places {
 // begins a unit, place 0: one that does not) and attn_join_kernel adds them in
 // order.  Without SPLIT a workgroup is a unit.
 //
-// A wave asks for its next pair before it works on one, across the border of two
-// segments too: the next segment's places are looked up while this one is worked on.
+// A wave asks for its next pair's keys as soon as it has the scores of this one's, and for
+// the values when it has added this one's, across the border of two segments too: the
+// next segment's places and queries are looked up while this one is worked on.
 template <int D, int KIND, bool FINE, bool SPLIT>
 __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   constexpr int XT = D / 16;
   __shared__ float part_o[ATTN_WAVES][XT][64][4];
+  __shared__ uint32_t queries[query_pieces(FINE) * D / 32][64][4];
   __shared__ float part_m[ATTN_WAVES][16], part_l[ATTN_WAVES][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15;
   const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio), units = heads * tiles;
@@ -496,22 +541,38 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   Wave<D, KIND, FINE> w;
   w.lane = lane;
   Places at, at_ahead;
-  auto load = [&](Pair<D, KIND>& t, const Segment& s, const Places& p, int k, bool used) {
+  auto locate = [&](const Segment& s, const Places& p, int k) {  // the wave's pair k
     const int head = s.unit / tiles;
-    const uint8_t* codes = a.data + a.cache.tile(head, 0);
-    const uint8_t* scales = a.data + a.cache.scales(head, 0);
+    Where to;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const size_t page = (size_t)__builtin_amdgcn_readlane(p.page[i], k & 63) * a.cache.page_bytes;
+      const uint8_t* page = a.data + (size_t)__builtin_amdgcn_readlane(p.page[i], k & 63) * a.cache.page_bytes;
       const int in = __builtin_amdgcn_readlane(p.tile[i], k & 63);
-      t.load(i, codes + page + (size_t)in * 2 * kv_half_bytes(KIND, D), scales + page + (size_t)in * kv_scale_bytes(KIND, D), used ? lane : 0);
+      to.tile[i] = page + a.cache.tile(head, in);
+      to.scales[i] = page + a.cache.scales(head, in);
     }
+    return to;
   };
-  Pair<D, KIND> even, odd;
+  auto first_head = [&](const Segment& s) { return s.unit / tiles * ratio + s.unit % tiles * 16; };
+  auto columns = [&](const Segment& s) { const int c = ratio - s.unit % tiles * 16; return c < 16 ? c : 16; };
+  Queries<D, FINE> query;
+  auto ask = [&](const Segment& s) {
+    const size_t row = ((size_t)s.b * a.q_heads + first_head(s) + col) * D;
+    query.load(col < columns(s) ? static_cast<const uint8_t*>(a.q) + row * (a.q_dtype == 2 ? 2 : 4) : nullptr, a.q_dtype, wave, lane);
+  };
+  Half<D, KIND, false> keys;
+  Half<D, KIND, true> values;
   at.bad = false;
   at.look(a, g, wave, lane, 0, tpp);
+  ask(g);
   at.check(a);
-  load(even, g, at, 0, true);
+  {
+    const Where first = locate(g, at, 0);
+    query.put(queries, a.q_dtype, wave, lane);
+    keys.load(first, lane);
+    values.load(first, lane);
+  }
+  __syncthreads();
   while (true) {
     bool more = SPLIT && left > 0;
     Segment ahead = g;
@@ -521,7 +582,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
       if (unit == units) {
         unit = 0;
         do {
-          if (++seq >= a.B) return;  // not reached: `left` pairs are there
+          if (++seq >= a.B) return;  // not reached: what is left of the share lies in units
           sp = lengths.span(a, seq);
         } while (sp.pairs() == 0);
       }
@@ -534,40 +595,40 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     }
     at_ahead.bad = false;
     at_ahead.look(a, ahead, wave, lane, 0, tpp);
-    const int q0 = g.unit / tiles * ratio + g.unit % tiles * 16;
-    const int cols = ratio - g.unit % tiles * 16 < 16 ? ratio - g.unit % tiles * 16 : 16;
-    const size_t q_row = ((size_t)g.b * a.q_heads + q0 + col) * D;
-    w.queries(col < cols ? static_cast<const uint8_t*>(a.q) + q_row * (a.q_dtype == 2 ? 2 : 4) : nullptr, a.q_dtype);
+    if (more) ask(ahead);
+    const int cols = columns(g);
+    const size_t q_row = ((size_t)g.b * a.q_heads + first_head(g) + col) * D;
     w.begin();
     const int count = g.p1 - g.p0 > wave ? (g.p1 - g.p0 - wave + ATTN_WAVES - 1) / ATTN_WAVES : 0;
-    auto take = [&](Pair<D, KIND>& t, int k) {
-      w.step(t, c, (g.sp.first_pair() + g.p0 + wave + k * ATTN_WAVES) * ATTN_PAIR, g.sp.lo, g.sp.n);
-    };
-    // the wave's pair k, or the next segment's first, or (no such) a few lines again: a load
-    // that may be left out would make the compiler wait for all of them
-    auto load_behind = [&](Pair<D, KIND>& t, int k) {
-      if (k < count) {
-        if ((k & 63) == 0) {
-          at.look(a, g, wave, lane, k, tpp);
+    for (int k = 0; k < count; k++) {
+      const int first = (g.sp.first_pair() + g.p0 + wave + k * ATTN_WAVES) * ATTN_PAIR;
+      float x[8];
+      w.scores(keys, queries, c, x);
+      // the wave's pair k + 1, or the next segment's first, or (no such) a few lines again: a
+      // load that may be left out would make the compiler wait for all of them
+      Where next;
+      if (k + 1 < count) {
+        if (((k + 1) & 63) == 0) {
+          at.look(a, g, wave, lane, k + 1, tpp);
           at.check(a);
         }
-        load(t, g, at, k, true);
+        next = locate(g, at, k + 1);
       } else {
         at_ahead.check(a);
-        load(t, ahead, at_ahead, 0, more);
+        next = locate(ahead, at_ahead, 0);
       }
-      __builtin_amdgcn_sched_barrier(0);
-    };
+      const int reader = more || k + 1 < count ? lane : 0;
+      keys.load(next, reader);
+      uint32_t keep[4];
+      w.weigh(x, first, g.sp.lo, g.sp.n, keep);
+      w.add(values, x, keep, first < g.sp.lo || first + ATTN_PAIR > g.sp.n);
+      values.load(next, reader);
+    }
     if (count == 0 && more) {
       at_ahead.check(a);
-      load(even, ahead, at_ahead, 0, true);
-    }
-    for (int k = 0; k < count; k += 2) {
-      load_behind(odd, k + 1);
-      take(even, k);
-      if (k + 1 == count) break;
-      load_behind(even, k + 2);
-      take(odd, k + 1);
+      const Where next = locate(ahead, at_ahead, 0);
+      keys.load(next, lane);
+      values.load(next, lane);
     }
     w.l += __shfl_xor(w.l, 16);
     w.l += __shfl_xor(w.l, 32);
@@ -580,6 +641,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     }
 #pragma unroll
     for (int x = 0; x < XT; x++) *reinterpret_cast<v4f*>(part_o[wave][x][lane]) = w.o[x];
+    if (more) query.put(queries, a.q_dtype, wave, lane);
     __syncthreads();
     float m = NEG_INF, f[ATTN_WAVES], l = 0.0f;
 #pragma unroll
@@ -609,7 +671,6 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
       place[16 * D + 16 + lane] = l;
     }
     if (!more) return;
-    if (count & 1) even = odd;
     g = ahead;
     at = at_ahead;
   }

@@ -147,25 +147,54 @@ __device__ __forceinline__ void head_put(const HeadLanes<VEC, LG, C>& l, T* row,
   }
 }
 
-// The weights plus their offset, or ones.
+// The weights plus their offset, or ones: asked for by load(), so that nothing waits for
+// them before it has to.
+template <int VEC, int LG, int C>
+struct HeadWeights {
+  HeadRow<float, VEC, LG, C> wide;
+  HeadRow<uint16_t, VEC, LG, C> narrow;
+  int dtype;  // -1: none
+  __device__ __forceinline__ void load(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, const void* w) {
+    dtype = w && a.norm ? a.param_dtype : -1;
+    if (dtype == 0) wide.load(l, static_cast<const float*>(w), 0, true);
+    else if (dtype > 0) narrow.load(l, static_cast<const uint16_t*>(w), 0, true);
+  }
+  __device__ __forceinline__ void get(const HeadLanes<VEC, LG, C>& l, float offset, float (&v)[2 * VEC * C]) const {
+    if (dtype == 0) {
+      wide.get(l, v);
+    } else if (dtype == 1) {
+      HeadRow<_Float16, VEC, LG, C> half;
+      if constexpr (VEC == 4) {
+        half.a.u = narrow.a.u;
+        half.b.u = narrow.b.u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * VEC * C; i++) half.one[i] = __builtin_bit_cast(_Float16, narrow.one[i]);
+      }
+      half.get(l, v);
+    } else if (dtype == 2) {
+      narrow.get(l, v);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * VEC * C; i++) v[i] = dtype < 0 ? 1.0f : v[i] + offset;
+  }
+};
+
+// The same at once.
 template <int VEC, int LG, int C>
 __device__ __forceinline__ void head_weights(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, const void* w,
                                              float (&v)[2 * VEC * C]) {
-  if (!w || !a.norm) {
-#pragma unroll
-    for (int i = 0; i < 2 * VEC * C; i++) v[i] = 1.0f;
-    return;
-  }
+  const int dtype = w && a.norm ? a.param_dtype : -1;
   auto as = [&](auto t) {
     HeadRow<decltype(t), VEC, LG, C> r;
     r.load(l, static_cast<const decltype(t)*>(w), 0, true);
     r.get(l, v);
   };
-  if (a.param_dtype == 0) as(float{});
-  else if (a.param_dtype == 1) as(_Float16{});
-  else as(uint16_t{});
+  if (dtype == 0) as(float{});
+  else if (dtype == 1) as(_Float16{});
+  else if (dtype == 2) as(uint16_t{});
 #pragma unroll
-  for (int i = 0; i < 2 * VEC * C; i++) v[i] += a.weight_offset;
+  for (int i = 0; i < 2 * VEC * C; i++) v[i] = dtype < 0 ? 1.0f : v[i] + a.weight_offset;
 }
 
 // Orders a wave's accesses to shared memory between its lanes: LDS takes them in turn.
@@ -175,38 +204,55 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Cosine and sine of a lane's pairs at token t.  A wave's lanes form one pair's each
-// (those of one head's, where its slots would form them again for every head) and
-// pass them on through `shared`, the wave's own 2 x (LG VEC C) floats.
+// Cosines and sines of one token.  A wave's lanes form one pair's each (those of one
+// head's, where its slots would form them again for every head): load() asks for what
+// they are made of, get() makes them and passes them on through `shared`, the wave's
+// own 2 x (LG VEC C) floats.
 template <int VEC, int LG, int C>
-__device__ __forceinline__ void head_angles(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, int t, float* shared,
-                                            float (&c)[VEC * C], float (&s)[VEC * C]) {
-  constexpr int N = LG * VEC * C;
+struct HeadAngles {
+  static constexpr int N = LG * VEC * C, EACH = (N + 63) / 64;
+  int64_t position[EACH];
+  double freq[EACH];
+  __device__ __forceinline__ void load(const HeadLanes<VEC, LG, C>& l, const HeadArgs& a, int t) {
 #pragma unroll
-  for (int i = 0; i < (N + 63) / 64; i++) {
-    const int p = 64 * i + (threadIdx.x & 63);
-    if (p < l.half) {
-      const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
-      double u = (double)a.positions[(size_t)axis * a.tokens + t] * a.inv_freq[p] * 0.15915494309189533577;
+    for (int i = 0; i < EACH; i++) {
+      const int p = 64 * i + (threadIdx.x & 63);
+      position[i] = 0;
+      freq[i] = 0.0;
+      if (p < l.half) {
+        const int axis = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);
+        position[i] = a.positions[(size_t)axis * a.tokens + t];
+        freq[i] = a.inv_freq[p];
+      }
+    }
+  }
+  __device__ __forceinline__ void get(const HeadLanes<VEC, LG, C>& l, float* shared, float (&c)[VEC * C], float (&s)[VEC * C]) const {
+#pragma unroll
+    for (int i = 0; i < EACH; i++) {
+      const int p = 64 * i + (threadIdx.x & 63);
+      if (64 * i >= l.half) break;
+      double u = (double)position[i] * freq[i] * 0.15915494309189533577;
       u -= rint(u);
       float sine, cosine;
       sincospif((float)(2.0 * u), &sine, &cosine);
-      shared[p] = cosine;
-      shared[N + p] = sine;
+      if (p < l.half) {
+        shared[p] = cosine;
+        shared[N + p] = sine;
+      }
     }
-  }
-  wave_fence();
+    wave_fence();
 #pragma unroll
-  for (int i = 0; i < VEC * C; i++) {
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (l.turned(i)) {
-      c[i] = shared[l.pair(i)];
-      s[i] = shared[N + l.pair(i)];
+    for (int i = 0; i < VEC * C; i++) {
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+      if (l.turned(i)) {
+        c[i] = shared[l.pair(i)];
+        s[i] = shared[N + l.pair(i)];
+      }
     }
+    wave_fence();
   }
-  wave_fence();
-}
+};
 
 // Sum over the LG lanes of a head, to each of them, in a fixed order.
 template <int LG>
@@ -253,14 +299,26 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
     to.load(l, row, u * a.D, u < (kind ? a.k_heads : a.q_heads));
   };
   HeadRow<T, VEC, LG, C> next;
+  HeadAngles<VEC, LG, C> angles;
+  HeadWeights<VEC, LG, C> wq, wk;
+  const int last = part + (rounds - 1 - part) / parts * parts;  // keys there, or not at all
+  angles.load(l, a, t);
+  int64_t in = -1;
+  if (WRITE && last >= rq) in = a.slots[t];
   fetch(next, part);
-  float wq[2 * N], wk[2 * N], c[N], s[N];
-  head_weights(l, a, a.w_q, wq);
-  head_weights(l, a, a.w_k, wk);
-  KvPlace at{nullptr, 0, 0};
-  if (WRITE) at = kv_place(a.cache, a.data, a.slots[t]);
-  head_angles(l, a, t, turns[wave], c, s);
+  if (part < rq) wq.load(l, a, a.w_q);
+  if (last >= rq) wk.load(l, a, a.w_k);
+  float c[N], s[N], w[2 * N];
+  angles.get(l, turns[wave], c, s);
+  const KvPlace at = WRITE && last >= rq ? kv_place(a.cache, a.data, in) : KvPlace{nullptr, 0, 0};
+  bool keys = part >= rq;
+  if (keys) wk.get(l, a.weight_offset, w);
+  else wq.get(l, a.weight_offset, w);
   for (int k = part; k < rounds; k += parts) {
+    if (!keys && k >= rq) {
+      keys = true;
+      wk.get(l, a.weight_offset, w);
+    }
     const int kind = (k >= rq) + (k >= rq + rk), u = (k - (kind ? rq : 0) - (kind == 2 ? rk : 0)) * SLOTS + slot;
     const bool on = u < (kind ? a.k_heads : a.q_heads);
     float x[2 * N], y[2 * N];
@@ -273,7 +331,7 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
       for (int i = 0; i < 2 * N; i++) ss = fmaf(x[i], x[i], ss);
       r = 1.0f / sqrtf(head_sum<LG>(ss) / (float)a.D + a.eps);
 #pragma unroll
-      for (int i = 0; i < 2 * N; i++) y[i] = x[i] * r * (kind ? wk[i] : wq[i]);
+      for (int i = 0; i < 2 * N; i++) y[i] = x[i] * r * w[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 2 * N; i++) y[i] = x[i];
@@ -331,7 +389,9 @@ __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
   for (long long job = (long long)blockIdx.x * 16 + wave; job < jobs; job += (long long)gridDim.x * 16) {
     const int t = (int)(job / parts), part = (int)(job % parts);
     float c[N], s[N];
-    head_angles(l, a, t, red[wave], c, s);
+    HeadAngles<VEC, LG, C> angles;
+    angles.load(l, a, t);
+    angles.get(l, red[wave], c, s);
 #pragma unroll
     for (int kind = 0; kind < 2; kind++) {
       const int heads = kind ? a.k_heads : a.q_heads, step = parts * SLOTS;
