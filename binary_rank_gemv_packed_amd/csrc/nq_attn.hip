@@ -39,7 +39,12 @@ typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int ATTN_WAVES = 4;
-constexpr int ATTN_GRID = 512;    // workgroups that share the tokens of all sequences
+constexpr int ATTN_GRID_MAX = 768;
+// Workgroups that share the tokens of all sequences: as many as a chip of 256 CUs holds at
+// once.  Three a CU for bf16 results of 4-bit caches, whose registers allow it and whose vector
+// and matrix instructions it overlaps (1 x 131072 46.6 -> 43.6 us); two elsewhere: 8 bits 54.9 us
+// against 57.7 with three, bf16 96.7 and 100.0.
+constexpr int attn_grid(int D, int kind, bool fine) { return kind == KV_INT4 && !fine && D <= 128 ? 768 : 512; }
 constexpr int ATTN_PAIR = 32;     // tokens of a wave's step: two tiles
 constexpr int ATTN_TURN = 8;      // what a unit costs beside its pairs, in pairs
 constexpr float ATTN_RISE = 8.0f;  // a maximum is raised by more than this (powers of two)
@@ -134,8 +139,8 @@ struct Counts {
 };
 
 // A workgroup's share of `total`: at least a pair a wave.
-__device__ __forceinline__ long long share_of(long long total) {
-  const long long even = (total + ATTN_GRID - 1) / ATTN_GRID;
+__device__ __forceinline__ long long share_of(long long total, int grid) {
+  const long long even = (total + grid - 1) / grid;
   return even < ATTN_WAVES ? ATTN_WAVES : even;
 }
 
@@ -172,16 +177,20 @@ struct Where {
 
 // A pair's keys or values, and the scales of the lane's four slots of either tile,
 // NG groups, two words each.
-template <int D, int KIND, bool VALUE>
+// NARROW (up to eight query heads a key head): columns 8 .. 15 of the MFMA hold no head, and
+// the lanes there take over the second tile's scores of head L & 7; a lane then needs the
+// scales of one tile.
+template <int D, int KIND, bool VALUE, bool NARROW>
 struct Half {
-  static constexpr int LB = kv_lane_bytes(KIND, D), NG = kv_groups(KIND, D);
-  uint32_t w[2][LB / 4], s[2][NG ? 2 * NG : 1];
+  static constexpr int LB = kv_lane_bytes(KIND, D), NG = kv_groups(KIND, D), TILES = NARROW ? 1 : 2;
+  uint32_t w[2][LB / 4], s[TILES][NG ? 2 * NG : 1];
   // lane: where no pair is left every lane reads lane 0's part, a line of each piece
   __device__ __forceinline__ void load(const Where& at, int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-      lane_bytes<LB>(at.tile[i] + (VALUE ? kv_half_bytes(KIND, D) : 0), lane, w[i]);
-      const uint8_t* q = at.scales[i] + (lane >> 4) * 16 * NG + (VALUE ? 8 * NG : 0);
+    for (int i = 0; i < 2; i++) lane_bytes<LB>(at.tile[i] + (VALUE ? kv_half_bytes(KIND, D) : 0), lane, w[i]);
+#pragma unroll
+    for (int i = 0; i < TILES; i++) {
+      const uint8_t* q = (NARROW ? lane & 8 ? at.scales[1] : at.scales[0] : at.scales[i]) + (lane >> 4) * 16 * NG + (VALUE ? 8 * NG : 0);
 #pragma unroll
       for (int p = 0; p < NG / 2; p++) {
         const u32x4 u = *reinterpret_cast<const u32x4_at4*>(q + 16 * p);
@@ -290,9 +299,19 @@ struct Queries {
   }
 };
 
-template <int D, int KIND, bool FINE>
+// The lanes of columns 0 .. 7 of `low`, and in columns 8 .. 15 what `high` has eight lanes before.
+__device__ __forceinline__ float two_tiles(float low, float high) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(low), __float_as_int(high), 0x118, 0xf, 0xc, false));
+}
+// What the lane eight columns on has (zero in columns 8 .. 15).
+__device__ __forceinline__ uint32_t eight_on(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x108, 0xf, 0xf, true);
+}
+
+template <int D, int KIND, bool FINE, bool NARROW>
 struct Wave {
   static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE);
+  static constexpr int TILES = NARROW ? 1 : 2, X = 4 * TILES;  // scores of a lane
   static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24
   v4f o[XT];
   float m, safe, l;
@@ -306,8 +325,8 @@ struct Wave {
     for (int x = 0; x < XT; x++) o[x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  // the scores (in powers of two) of the lane's 2 x 4 tokens of its head
-  __device__ __forceinline__ void scores(const Half<D, KIND, false>& t, const uint32_t (*q)[64][4], float c, float (&x)[8]) const {
+  // the scores (in powers of two) of the lane's 2 x 4 tokens (NARROW: 4) of its head
+  __device__ __forceinline__ void scores(const Half<D, KIND, false, NARROW>& t, const uint32_t (*q)[64][4], float c, float (&x)[X]) const {
     const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
     v4f s[2];
     s[0] = s[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -316,60 +335,66 @@ struct Wave {
       u32x4 query[PIECES];
 #pragma unroll
       for (int p = 0; p < PIECES; p++) query[p] = *reinterpret_cast<const u32x4*>(q[p * CH + ch][lane]);
-      v4f less = {0.0f, 0.0f, 0.0f, 0.0f};
+      v4f less = {0.0f, 0.0f, 0.0f, 0.0f}, d[2];
       if constexpr (BIAS) less = mfma(minus, query[0], less);
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         const u32x4 key = t.template keys<FINE>(i, ch, nb);
-        v4f d = KIND == KV_INT4 ? less : s[i];
+        d[i] = KIND == KV_INT4 ? less : s[i];
 #pragma unroll
-        for (int p = PIECES - 1; p >= 0; p--) d = mfma(key, query[p], d);
-        if constexpr (KIND == KV_INT4) {
+        for (int p = PIECES - 1; p >= 0; p--) d[i] = mfma(key, query[p], d[i]);
+        if constexpr (KIND != KV_INT4) s[i] = d[i];
+      }
+      if constexpr (KIND == KV_INT4) {
 #pragma unroll
-          for (int j = 0; j < 4; j++) s[i][j] = fmaf(t.scale(i, ch, j), d[j], s[i][j]);
-        } else {
-          s[i] = d;
-        }
+        for (int i = 0; i < TILES; i++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) s[i][j] = fmaf(t.scale(i, ch, j), NARROW ? two_tiles(d[0][j], d[1][j]) : d[i][j], s[i][j]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      if constexpr (KIND == KV_INT8) x[j] = s[j / 4][j & 3] * (c * t.scale(j / 4, 0, j & 3));
-      else x[j] = s[j / 4][j & 3] * c;
+    for (int j = 0; j < X; j++) {
+      x[j] = s[j / 4][j & 3];
+      if constexpr (NARROW && KIND != KV_INT4) x[j] = two_tiles(s[0][j], s[1][j]);
+      x[j] *= KIND == KV_INT8 ? c * t.scale(j / 4, 0, j & 3) : c;
     }
   }
 
   // Scores to weights.  32 tokens from `first` on, of which those from lo to n - 1 are seen:
   // the others weigh nothing and `keep` masks their values (bf16) or scales, for what
   // lies there may be anything.
-  __device__ __forceinline__ void weigh(float (&x)[8], int first, int lo, int n, uint32_t (&keep)[4]) {
+  __device__ __forceinline__ void weigh(float (&x)[X], int first, int lo, int n, uint32_t (&keep)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; i++) keep[i] = ~0u;
     if (first < lo || first + ATTN_PAIR > n) {
       asm volatile("");  // a branch: made into selects this costs 45 instructions a step
+      const int at = first + 4 * (lane >> 4);
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const int at = first + j / 4 * 16 + 4 * (lane >> 4) + (j & 3);
-        if (at < lo || at >= n) {
-          x[j] = NEG_INF;
-          keep[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
-        }
+      for (int j = 0; j < X; j++) {
+        const int token = at + (NARROW ? 2 * (lane & 8) : j / 4 * 16) + (j & 3);
+        if (token < lo || token >= n) x[j] = NEG_INF;
+      }
+      // bf16 values of both tiles; scales of the lane's own
+#pragma unroll
+      for (int j = 0; j < (KIND == KV_BF16 ? 8 : X); j++) {
+        const int token = at + (NARROW && KIND != KV_BF16 ? 2 * (lane & 8) : j / 4 * 16) + (j & 3);
+        if (token < lo || token >= n) keep[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
       }
     }
     float top = NEG_INF;
 #pragma unroll
-    for (int j = 0; j < 8; j++) top = fmaxf(top, x[j]);
+    for (int j = 0; j < X; j++) top = fmaxf(top, x[j]);
     if (__any(top > m + ATTN_RISE)) raise(top);
 #pragma unroll
-    for (int j = 0; j < 8; j++) x[j] = __builtin_amdgcn_exp2f(x[j] - safe);
+    for (int j = 0; j < X; j++) x[j] = __builtin_amdgcn_exp2f(x[j] - safe);
   }
 
-  __device__ __forceinline__ void add(Half<D, KIND, true>& t, const float (&p)[8], const uint32_t (&keep)[4], bool edge) {
+  __device__ __forceinline__ void add(Half<D, KIND, true, NARROW>& t, const float (&p)[X], const uint32_t (&keep)[4], bool edge) {
     if constexpr (NG == 0) {
       u32x4 w[PIECES];
       weights(p, w);
 #pragma unroll
-      for (int j = 0; j < 4; j++) l += FINE ? p[2 * j] + p[2 * j + 1] : low_f32(w[0][j]) + high_f32(w[0][j]);
+      for (int j = 0; j < X / 2; j++) l += FINE ? p[2 * j] + p[2 * j + 1] : low_f32(w[0][j]) + high_f32(w[0][j]);
 #pragma unroll
       for (int x = 0; x < XT; x++) {
         const u32x4 value = t.template values<FINE>(x, keep, nb);
@@ -380,17 +405,17 @@ struct Wave {
       if (edge) {
         asm volatile("");
 #pragma unroll
-        for (int i = 0; i < 2; i++)
+        for (int i = 0; i < TILES; i++)
 #pragma unroll
           for (int k = 0; k < 2 * NG; k++) t.s[i][k] &= keep[2 * i + (k & 1)];
       }
 #pragma unroll
-      for (int j = 0; j < 8; j++) l += p[j];
+      for (int j = 0; j < X; j++) l += p[j];
 #pragma unroll
       for (int g = 0; g < NG; g++) {
-        float ps[8];
+        float ps[X];
 #pragma unroll
-        for (int j = 0; j < 8; j++) ps[j] = p[j] * t.scale(j / 4, g, j & 3);
+        for (int j = 0; j < X; j++) ps[j] = p[j] * t.scale(j / 4, g, j & 3);
         u32x4 w[PIECES];
         weights(ps, w);
 #pragma unroll
@@ -408,15 +433,16 @@ struct Wave {
   }
 
   // weights as bf16, or as pieces that add up to them
-  __device__ __forceinline__ static void weights(const float (&p)[8], u32x4 (&w)[PIECES]) {
+  __device__ __forceinline__ static void weights(const float (&p)[X], u32x4 (&w)[PIECES]) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < X / 2; j++) {
       float lo = p[2 * j], hi = p[2 * j + 1];
 #pragma unroll
       for (int i = 0; i < PIECES; i++) {
         w[i][j] = pack_bf16(lo, hi);
         lo -= low_f32(w[i][j]);
         hi -= high_f32(w[i][j]);
+        if constexpr (NARROW) w[i][2 + j] = eight_on(w[i][j]);  // the second tile's, in the other half of the columns
       }
     }
   }
@@ -424,6 +450,7 @@ struct Wave {
   __device__ __forceinline__ void raise(float top) {
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
+    if constexpr (NARROW) top = fmaxf(top, __shfl_xor(top, 8));
     const float to = fmaxf(m, top);
     const float f = to == m ? 1.0f : __builtin_amdgcn_exp2f(m - to);
     m = to;
@@ -490,7 +517,7 @@ struct Places {
 // A wave asks for its next pair's keys as soon as it has the scores of this one's, and for
 // the values when it has added this one's, across the border of two segments too: the
 // next segment's places and queries are looked up while this one is worked on.
-template <int D, int KIND, bool FINE, bool SPLIT>
+template <int D, int KIND, bool FINE, bool NARROW, bool SPLIT>
 __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   constexpr int XT = D / 16;
   __shared__ float part_o[ATTN_WAVES][XT][64][4];
@@ -505,7 +532,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   long long left;  // what this workgroup's share holds behind g
   if constexpr (SPLIT) {
     const Counts n(a, lengths);
-    const long long total = (long long)n.total * units, share = share_of(total), start = share * blockIdx.x;
+    const long long total = (long long)n.total * units, share = share_of(total, attn_grid(D, KIND, FINE)), start = share * blockIdx.x;
     if (start >= total) return;
     left = total - start < share ? total - start : share;
     const bool here = start >= (long long)n.before * units && start < ((long long)n.before + n.mine) * units;
@@ -538,7 +565,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
       return;
     }
   }
-  Wave<D, KIND, FINE> w;
+  Wave<D, KIND, FINE, NARROW> w;
   w.lane = lane;
   Places at, at_ahead;
   auto locate = [&](const Segment& s, const Places& p, int k) {  // the wave's pair k
@@ -560,8 +587,8 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     const size_t row = ((size_t)s.b * a.q_heads + first_head(s) + col) * D;
     query.load(col < columns(s) ? static_cast<const uint8_t*>(a.q) + row * (a.q_dtype == 2 ? 2 : 4) : nullptr, a.q_dtype, wave, lane);
   };
-  Half<D, KIND, false> keys;
-  Half<D, KIND, true> values;
+  Half<D, KIND, false, NARROW> keys;
+  Half<D, KIND, true, NARROW> values;
   at.bad = false;
   at.look(a, g, wave, lane, 0, tpp);
   ask(g);
@@ -602,7 +629,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     const int count = g.p1 - g.p0 > wave ? (g.p1 - g.p0 - wave + ATTN_WAVES - 1) / ATTN_WAVES : 0;
     for (int k = 0; k < count; k++) {
       const int first = (g.sp.first_pair() + g.p0 + wave + k * ATTN_WAVES) * ATTN_PAIR;
-      float x[8];
+      float x[NARROW ? 4 : 8];
       w.scores(keys, queries, c, x);
       // the wave's pair k + 1, or the next segment's first, or (no such) a few lines again: a
       // load that may be left out would make the compiler wait for all of them
@@ -632,6 +659,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     }
     w.l += __shfl_xor(w.l, 16);
     w.l += __shfl_xor(w.l, 32);
+    if constexpr (NARROW) w.l += __shfl_xor(w.l, 8);
     if (__any(at.bad)) w.l = __uint_as_float(0x7fc00000u);
     // the waves' sums: every wave adds a share of the channels, in the order of the waves
     __syncthreads();
@@ -680,7 +708,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
 // D / 4 threads go through the parts of a head that fall to their group of them, eight
 // parts in flight, and the groups' sums are added in order.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int hb, int blocks) {
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, int hb, int blocks) {
   constexpr int Q = D / 4, SLOTS = 256 / Q, N = 8;
   __shared__ v4f sums[SLOTS][Q];
   __shared__ float slot_m[SLOTS], slot_l[SLOTS];
@@ -703,7 +731,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int hb, int 
   }
   int front = __builtin_amdgcn_readlane(n.before, b / n.each);
   for (int i = b / n.each * n.each; i < b; i++) front += span_of(a, a.lengths[i]).cost();
-  const long long share = share_of((long long)n.total * units);
+  const long long share = share_of((long long)n.total * units, grid);
   const long long start = (long long)front * units + (long long)unit * (pairs + ATTN_TURN) + ATTN_TURN;
   const int w0 = (int)(start / share), parts = (int)((start + pairs - 1) / share) - w0 + 1;
   if (parts == 1) return;
@@ -759,41 +787,43 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int hb, int 
 }
 
 // ------------------------------------------------------------------ host
-template <int D, int KIND, bool FINE>
+template <int D, int KIND, bool FINE, bool NARROW>
 void attn_launch(const AttnArgs& a) {
   const int heads = a.cache.heads, units = heads * head_tiles(a.q_heads / heads);
-  // Units as they are, a workgroup each, where none is long, or there are many and none very
-  // long: no join (some 6 us with its launch), but a long unit beside short ones is one
-  // workgroup's.  8 key heads of 128, 8 bits, one launch and two: 16 x 1024 tokens 13.8 and 18.2
-  // us, 64 x 2048 48.2 and 54.7, 16 x 2048 23.0 and 23.3, 1 x 1024 12.1 and 10.7, 1 x 2048 20.0 and 11.4.
+  constexpr int grid = attn_grid(D, KIND, FINE);
+  // Units as they are, a workgroup each, where none is long: no join (some 6 us with its
+  // launch), but a long unit beside short ones is one workgroup's.  8 key heads of 128, 8 bits,
+  // one launch and two: 16 x 1024 tokens 13.8 and 18.2 us, 1 x 1024 12.1 and 10.7, 64 x 2048 48.2
+  // and 54.7, but 64 of 16 to 4096 tokens (spread over the logarithm) 38.7 and 29.3.
   const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
-  if (longest <= 1024 || (longest <= 2048 && (long long)a.B * units >= ATTN_GRID)) {
-    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, false>), dim3((unsigned)(a.B * units)), dim3(64 * ATTN_WAVES), 0, a.stream, a);
+  if (longest <= 1024) {
+    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false>), dim3((unsigned)(a.B * units)), dim3(64 * ATTN_WAVES), 0, a.stream, a);
     return;
   }
-  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, true>), dim3(ATTN_GRID), dim3(64 * ATTN_WAVES), 0, a.stream, a);
+  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
   // Heads of a workgroup of the join: one where there are few, else as many as leave the
   // longest unit (all tokens in one sequence) 64 parts a group at most.  With one head each
   // 64 sequences of 64 heads take 11.9 us instead of 5.8.
   constexpr int SLOTS = 256 / (D / 4);
-  const int ratio = a.q_heads / heads, most = ratio < 16 ? ratio : 16, groups = (ATTN_GRID / units + 2 + 63) / 64;
+  const int ratio = a.q_heads / heads, most = ratio < 16 ? ratio : 16, groups = (grid / units + 2 + 63) / 64;
   int hb = a.B * a.q_heads <= 512 || groups >= SLOTS ? 1 : SLOTS / groups;
   hb = hb < most ? hb : most;
   const int blocks = (most + hb - 1) / hb;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, hb, blocks);
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, hb, blocks);
 }
 
 template <int D>
 void attn_by_kind(const AttnArgs& a) {
   const bool fine = a.q_dtype == 0 || a.y_dtype == 0;
-  if (a.cache.kind == KV_BF16) fine ? attn_launch<D, KV_BF16, true>(a) : attn_launch<D, KV_BF16, false>(a);
-  else if (a.cache.kind == KV_INT8) fine ? attn_launch<D, KV_INT8, true>(a) : attn_launch<D, KV_INT8, false>(a);
-  else fine ? attn_launch<D, KV_INT4, true>(a) : attn_launch<D, KV_INT4, false>(a);
+  if (a.cache.kind == KV_BF16) fine ? attn_launch<D, KV_BF16, true, false>(a) : attn_launch<D, KV_BF16, false, false>(a);
+  else if (a.cache.kind == KV_INT8) fine ? attn_launch<D, KV_INT8, true, false>(a) : attn_launch<D, KV_INT8, false, false>(a);
+  else if (a.q_heads / a.cache.heads <= 8) fine ? attn_launch<D, KV_INT4, true, true>(a) : attn_launch<D, KV_INT4, false, true>(a);
+  else fine ? attn_launch<D, KV_INT4, true, false>(a) : attn_launch<D, KV_INT4, false, false>(a);
 }
 
 }  // namespace
 
-size_t attn_workspace(const KvLayout& l) { return align_up(ATTN_GRID * 2 * slot_floats(l.D) * 4, 256); }
+size_t attn_workspace(const KvLayout& l) { return align_up(ATTN_GRID_MAX * 2 * slot_floats(l.D) * 4, 256); }
 
 hipError_t attn_forward(const AttnArgs& a) {
   switch (a.cache.D) {
