@@ -482,7 +482,7 @@ struct Segment {
 // multiple of 64.  Behind the segment's last pair that one stands again.
 struct Places {
   int page[2], tile[2];
-  bool bad;
+  int bad;  // (not a bool, whose padding would take the copies through memory)
   __device__ __forceinline__ void look(const AttnArgs& a, const Segment& g, int wave, int lane, int k, int tpp) {
     int pair = g.p0 + wave + (k + lane) * ATTN_WAVES;
     pair = g.sp.first_pair() + (pair < g.p1 ? pair : g.p1 - 1);
@@ -502,7 +502,7 @@ struct Places {
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       const bool out = page[i] < 0 || page[i] >= a.cache.pages;
-      bad |= out;
+      bad |= out ? 1 : 0;
       page[i] = out ? 0 : page[i];
     }
   }
@@ -589,15 +589,15 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   };
   Half<D, KIND, false, NARROW> keys;
   Half<D, KIND, true, NARROW> values;
-  at.bad = false;
+  at.bad = 0;
   at.look(a, g, wave, lane, 0, tpp);
   ask(g);
   at.check(a);
   {
     const Where first = locate(g, at, 0);
-    query.put(queries, a.q_dtype, wave, lane);
     keys.load(first, lane);
     values.load(first, lane);
+    query.put(queries, a.q_dtype, wave, lane);
   }
   __syncthreads();
   while (true) {
@@ -620,9 +620,13 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
         more = false;
       }
     }
-    at_ahead.bad = false;
-    at_ahead.look(a, ahead, wave, lane, 0, tpp);
-    if (more) ask(ahead);
+    if (more) {
+      at_ahead.bad = 0;
+      at_ahead.look(a, ahead, wave, lane, 0, tpp);
+      ask(ahead);
+    } else {
+      at_ahead = at;
+    }
     const int cols = columns(g);
     const size_t q_row = ((size_t)g.b * a.q_heads + first_head(g) + col) * D;
     w.begin();
