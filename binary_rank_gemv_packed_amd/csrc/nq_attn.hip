@@ -21,6 +21,13 @@
 // FINE, for fp32 queries or outputs, takes weights and queries as three bf16 pieces,
 // exactly, and 4-bit codes as c, for 24 times the sum of the weights would cost some of
 // the bits that are asked for.
+//
+// Bound by memory where sequences are long: 32 of up to 16384 tokens (675 MB of bf16) 118
+// us with the join, 5.7 TB/s, where a large copy moves 5.2 and reads alone 6.9; 131072 tokens
+// of 8 bits 55 us, of which the join and its launch are 7 and the way to the first keys
+// (lengths, places, tiles, one access behind the other) 4; of 4 bits 43 us, where vector
+// instructions take half of the cycles and a wave still waits for a third of its own.  Heads of
+// 192 and 256 with FINE keep one workgroup a CU (shared memory).
 #include "nq_common.h"
 #include "nq_internal.h"
 
@@ -41,12 +48,16 @@ typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 constexpr int ATTN_WAVES = 4;
 constexpr int ATTN_GRID_MAX = 768;
 // Workgroups that share the tokens of all sequences: as many as a chip of 256 CUs holds at
-// once.  Three a CU for bf16 results of 4-bit caches, whose registers allow it and whose vector
-// and matrix instructions it overlaps (1 x 131072 46.6 -> 43.6 us); two elsewhere: 8 bits 54.9 us
-// against 57.7 with three, bf16 96.7 and 100.0.
-constexpr int attn_grid(int D, int kind, bool fine) { return kind == KV_INT4 && !fine && D <= 128 ? 768 : 512; }
+// once.  Three a CU for bf16 results of 4-bit caches (up to eight query heads a key head),
+// whose registers allow it and whose vector and matrix instructions it overlaps (131072 tokens
+// 46.6 -> 43.6 us); two elsewhere: 8 bits 54.9 us against 57.7 with three, bf16 96.7 and 100.0.
+constexpr int attn_grid(int D, int kind, bool fine, bool narrow) {
+  return kind == KV_INT4 && !fine && narrow && D <= 128 ? 768 : 512;
+}
 constexpr int ATTN_PAIR = 32;     // tokens of a wave's step: two tiles
-constexpr int ATTN_TURN = 8;      // what a unit costs beside its pairs, in pairs
+// What a unit costs beside its pairs (its queries, places and the waves' join), in pairs:
+// 64 sequences of 256 to 4096 tokens of 8 bits 57.0 us counted as 0, 49.8 as 4, 46.9 as 8, 47.5 as 12.
+constexpr int ATTN_TURN = 8;
 constexpr float ATTN_RISE = 8.0f;  // a maximum is raised by more than this (powers of two)
 #define NEG_INF (-__builtin_inff())
 
@@ -532,7 +543,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   long long left;  // what this workgroup's share holds behind g
   if constexpr (SPLIT) {
     const Counts n(a, lengths);
-    const long long total = (long long)n.total * units, share = share_of(total, attn_grid(D, KIND, FINE)), start = share * blockIdx.x;
+    const long long total = (long long)n.total * units, share = share_of(total, attn_grid(D, KIND, FINE, NARROW)), start = share * blockIdx.x;
     if (start >= total) return;
     left = total - start < share ? total - start : share;
     const bool here = start >= (long long)n.before * units && start < ((long long)n.before + n.mine) * units;
@@ -794,7 +805,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, in
 template <int D, int KIND, bool FINE, bool NARROW>
 void attn_launch(const AttnArgs& a) {
   const int heads = a.cache.heads, units = heads * head_tiles(a.q_heads / heads);
-  constexpr int grid = attn_grid(D, KIND, FINE);
+  constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
   // Units as they are, a workgroup each, where none is long: no join (some 6 us with its
   // launch), but a long unit beside short ones is one workgroup's.  8 key heads of 128, 8 bits,
   // one launch and two: 16 x 1024 tokens 13.8 and 18.2 us, 1 x 1024 12.1 and 10.7, 64 x 2048 48.2

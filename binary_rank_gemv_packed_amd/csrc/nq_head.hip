@@ -11,8 +11,10 @@
 //   t = g (w + o),  dx = r (t - x r mean(t x r)).
 //
 // The angle is formed in 64 bits, in turns, for positions are far (the product's
-// rounding is 2^-52 of it); its fraction of a turn, its sine and cosine and all
-// other arithmetic are fp32, and each output is rounded once, to its type.
+// rounding is 2^-52 of it), and in the forward so are its sine and cosine, rounded to fp32
+// (once a wave and pair: formed in fp32 they would cost an output another 2^-24 here and
+// there, which turns some of its bf16 roundings).  All other arithmetic is fp32, and each
+// output is rounded once, to its type.
 #include "nq_common.h"
 #include "nq_internal.h"
 
@@ -207,8 +209,9 @@ __device__ __forceinline__ void wave_fence() {
 // Cosines and sines of one token.  A wave's lanes form one pair's each (those of one
 // head's, where its slots would form them again for every head): load() asks for what
 // they are made of, get() makes them and passes them on through `shared`, the wave's
-// own 2 x (LG VEC C) floats.
-template <int VEC, int LG, int C>
+// own 2 x (LG VEC C) floats.  WIDE: in 64 bits, for the forward; the backward pass has no
+// registers for it.
+template <int VEC, int LG, int C, bool WIDE>
 struct HeadAngles {
   static constexpr int N = LG * VEC * C, EACH = (N + 63) / 64;
   int64_t position[EACH];
@@ -234,7 +237,18 @@ struct HeadAngles {
       double u = (double)position[i] * freq[i] * 0.15915494309189533577;
       u -= rint(u);
       float sine, cosine;
-      sincospif((float)(2.0 * u), &sine, &cosine);
+      if constexpr (WIDE) {
+        double sine64, cosine64;
+        sincospi(2.0 * u, &sine64, &cosine64);
+        sine = (float)sine64;
+        cosine = (float)cosine64;
+      } else {  // of the rounded angle, turned by what the rounding left
+        const float half = (float)(2.0 * u), rest = (float)(2.0 * u - (double)half) * 3.14159265f;
+        float s0, c0;
+        sincospif(half, &s0, &c0);
+        sine = fmaf(rest, c0, s0);
+        cosine = fmaf(-rest, s0, c0);
+      }
       if (p < l.half) {
         shared[p] = cosine;
         shared[N + p] = sine;
@@ -272,6 +286,9 @@ __device__ __forceinline__ float round_to(float v, const float*) { return v; }
 __device__ __forceinline__ float round_to(float v, const uint16_t*) { return to_f32<uint16_t>(f32_to_bf16(v)); }
 
 // ------------------------------------------------------------------ forward
+// Bound by memory where there are many tokens: 2048 of 64 + 8 heads of 128 in bf16 16.5 us
+// (4.6 TB/s), 30 us with an angle formed for every head; one token takes 3.5 us in a
+// graph, of which one access and the launch are some three.
 // A wave takes one token, or one of `parts` shares of a token's heads, so that the
 // angles are formed once for all of them; 64 / LG heads a round, the next round's
 // asked for before the present one's are worked on.  A round's heads are all queries, all
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
     to.load(l, row, u * a.D, u < (kind ? a.k_heads : a.q_heads));
   };
   HeadRow<T, VEC, LG, C> next;
-  HeadAngles<VEC, LG, C> angles;
+  HeadAngles<VEC, LG, C, true> angles;
   HeadWeights<VEC, LG, C> wq, wk;
   const int last = part + (rounds - 1 - part) / parts * parts;  // keys there, or not at all
   angles.load(l, a, t);
@@ -375,7 +392,9 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
 // Shares of tokens as in the forward; the waves of the grid take them in turn.  The
 // sums for both weights stay in registers over all of a wave's tokens and are joined
 // over a head's slots, the workgroup's waves and (head_join_kernel) the workgroups in
-// a fixed order.
+// a fixed order.  Bound by memory: 4096 tokens of 64 + 8 heads of 128 in bf16 47 us (4.8
+// TB/s) and the join 4 us.  Odd heads above 128 channels (VEC = 1, C = 4) spill 300 bytes a
+// lane: 2048 tokens of 24 heads of 510 in fp32 90 us, 3.3 TB/s.
 template <typename T, int VEC, int LG, int C>
 __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
   constexpr int N = VEC * C, SLOTS = 64 / LG, TURNS = 2 * LG * N;
@@ -389,7 +408,7 @@ __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
   for (long long job = (long long)blockIdx.x * 16 + wave; job < jobs; job += (long long)gridDim.x * 16) {
     const int t = (int)(job / parts), part = (int)(job % parts);
     float c[N], s[N];
-    HeadAngles<VEC, LG, C> angles;
+    HeadAngles<VEC, LG, C, false> angles;
     angles.load(l, a, t);
     angles.get(l, red[wave], c, s);
 #pragma unroll
@@ -516,6 +535,8 @@ int head_parts(int tokens, int rounds, int waves) {
   const int want = ceil_div(waves, tokens);
   return ceil_div(rounds, ceil_div(rounds, want < rounds ? want : rounds));
 }
+// Waves of the forward: 64 / 8 heads of 128, 2048 tokens of bf16 19.0 us with 6144 (three shares
+// of six rounds a token), 20.5 with 4096, 19.0 with 8192, 21.9 with 16384 (at that step).
 constexpr int HEAD_WAVES = 6144;
 
 template <typename Kind>

@@ -105,6 +105,28 @@ def test_heads(Hq, H, kind, long):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q", [BF, F32])
+def test_more_than_eight_query_heads_a_key_head(D, kind, q):
+    for lengths in ([33, 500, 0, 7], [2200, 3, 900]):
+        c = Case(lengths, 24, 2, D, 32, kind, q)
+        c.check(c.run())
+
+
+def test_many_sequences():
+    """More sequences than a wave has lanes, several times over, most of them empty, in one
+    launch and in two."""
+    lengths = [(7 * i) % 5 * (i % 3) for i in range(9001)]
+    lengths[8000] = 3000
+    c = Case(lengths, 2, 1, 64, 16, "int8", BF, F32)
+    some = list(range(0, 9001, 97)) + [7999, 8000, 8001, 9000]
+    c.check(c.run(), some)
+    c.gl[8000] = 17
+    c.lengths[8000], c.k[8000], c.v[8000] = 17, c.k[8000][:17], c.v[8000][:17]
+    c.check(c.run(max_length=64), some)
+
+
 @pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 1024])
 @pytest.mark.parametrize("kind", KINDS)
 def test_pages(page, kind):
