@@ -393,19 +393,21 @@ __global__ void __launch_bounds__(256) head_fwd_kernel(HeadArgs a, int parts) {
 // sums for both weights stay in registers over all of a wave's tokens and are joined
 // over a head's slots, the workgroup's waves and (head_join_kernel) the workgroups in
 // a fixed order.  Bound by memory: 4096 tokens of 64 + 8 heads of 128 in bf16 47 us (4.8
-// TB/s) and the join 4 us.  Odd heads above 128 channels (VEC = 1, C = 4) spill 300 bytes a
-// lane: 2048 tokens of 24 heads of 510 in fp32 90 us, 3.3 TB/s.
+// TB/s) and the join 4 us.  Odd heads above 128 channels (C = 4) take eight waves a
+// workgroup, which may have 256 registers each: 2048 tokens of 24 heads of 510 in fp32 75 us, where
+// sixteen with 128 registers spill 300 bytes a lane and take 90.
+constexpr int head_bwd_waves(int C) { return C == 4 ? 8 : 16; }
 template <typename T, int VEC, int LG, int C>
-__global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
-  constexpr int N = VEC * C, SLOTS = 64 / LG, TURNS = 2 * LG * N;
-  __shared__ float red[16][TURNS > HEAD_MAX_DIM ? TURNS : HEAD_MAX_DIM];  // first the waves' angles, then their sums
+__global__ void __launch_bounds__(64 * head_bwd_waves(C)) head_bwd_kernel(HeadArgs a, int parts) {
+  constexpr int N = VEC * C, SLOTS = 64 / LG, TURNS = 2 * LG * N, WAVES = head_bwd_waves(C);
+  __shared__ float red[WAVES][TURNS > HEAD_MAX_DIM ? TURNS : HEAD_MAX_DIM];  // first the waves' angles, then their sums
   const int lane = threadIdx.x & 63, slot = lane / LG, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const HeadLanes<VEC, LG, C> l{lane % LG, a.D, a.rot / 2, a.interleaved};
   float sums[2][2 * N];
 #pragma unroll
   for (int i = 0; i < 2 * N; i++) sums[0][i] = sums[1][i] = 0.0f;
   const long long jobs = (long long)a.tokens * parts;
-  for (long long job = (long long)blockIdx.x * 16 + wave; job < jobs; job += (long long)gridDim.x * 16) {
+  for (long long job = (long long)blockIdx.x * WAVES + wave; job < jobs; job += (long long)gridDim.x * WAVES) {
     const int t = (int)(job / parts), part = (int)(job % parts);
     float c[N], s[N];
     HeadAngles<VEC, LG, C, false> angles;
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(1024) head_bwd_kernel(HeadArgs a, int parts) {
     if ((int)threadIdx.x < a.D) {
       float v = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; i++) v += red[i][threadIdx.x];
+      for (int i = 0; i < WAVES; i++) v += red[i][threadIdx.x];
       a.part[((size_t)blockIdx.x * 2 + kind) * a.D + threadIdx.x] = v;
     }
   }
@@ -572,13 +574,13 @@ hipError_t head_backward(const HeadArgs& a) {
   int blocks = 0;
   if (a.tokens) {
     head_dispatch(a, [&](auto t, auto vec, auto lg, auto c) {
-      constexpr int LG = decltype(lg)::value;
+      constexpr int LG = decltype(lg)::value, C = decltype(c)::value, WAVES = head_bwd_waves(C);
       const int heads = a.q_heads > a.k_heads ? a.q_heads : a.k_heads;
-      const int parts = head_parts(a.tokens, ceil_div(heads, 64 / LG), 4096);
+      const int parts = head_parts(a.tokens, ceil_div(heads, 64 / LG), 256 * WAVES);
       const long long jobs = (long long)a.tokens * parts;
-      blocks = (int)(jobs < 256 * 16 ? (jobs + 15) / 16 : 256);
-      hipLaunchKernelGGL((head_bwd_kernel<decltype(t), decltype(vec)::value, LG, decltype(c)::value>), dim3(blocks),
-                         dim3(1024), 0, a.stream, a, parts);
+      blocks = (int)(jobs < 256 * WAVES ? (jobs + WAVES - 1) / WAVES : 256);
+      hipLaunchKernelGGL((head_bwd_kernel<decltype(t), decltype(vec)::value, LG, C>), dim3(blocks), dim3(64 * WAVES), 0,
+                         a.stream, a, parts);
     });
   }
   if (a.part || !a.tokens) hipLaunchKernelGGL(head_join_kernel, dim3(ceil_div(a.D, 64), 2), dim3(1024), 0, a.stream, a, blocks);
