@@ -445,8 +445,7 @@ nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots,
  * does not matter.  Asynchronous on `stream`, capturable (lengths and table are read by
  * the kernels); calls that overlap in time need workspaces of their own; repeated calls
  * give identical bits.  B == 0 launches nothing.  max_length and the window choose
- * between one launch (up to 1024 tokens, 2048 for large batches) and a split over the
- * length with a join. */
+ * between one launch (up to 1024 tokens) and a split over the length with a join. */
 size_t nq_kv_attention_workspace_bytes(const nq_kv_cache* C);
 nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_t q_dtype, int32_t q_heads,
                           const int32_t* table, int32_t table_width, const int32_t* lengths, int32_t max_length,
