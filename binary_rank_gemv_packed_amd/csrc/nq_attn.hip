@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     Span sp = lengths.span(a, b);
     while (from >= (long long)sp.cost() * units) {
       from -= (long long)sp.cost() * units;
-      sp = lengths.span(a, ++b);
+      if (++b >= a.B) return;  // not reached while the lengths stay as they were counted
+      sp = lengths.span(a, b);
     }
     const int unit = from < (1LL << 31) ? (int)((uint32_t)from / (uint32_t)sp.cost()) : (int)(from / sp.cost());
     from -= (long long)unit * sp.cost();
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
       l += f[i] * part_l[i][col];
     }
     const bool whole = g.p0 == 0 && g.p1 == g.sp.pairs();
-    const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+    const float inv = whole ? 1.0f / l : 1.0f;  // l is 0 where every score is -infinity: a NaN, as the formula's
     float* place = a.part + ((size_t)blockIdx.x * 2 + (g.p0 == 0)) * slot_floats(D);
     for (int x = wave; x < XT; x += ATTN_WAVES) {
       v4f s = *reinterpret_cast<const v4f*>(part_o[0][x][lane]) * f[0];
@@ -748,8 +749,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, in
   for (int i = b / n.each * n.each; i < b; i++) front += span_of(a, a.lengths[i]).cost();
   const long long share = share_of((long long)n.total * units, grid);
   const long long start = (long long)front * units + (long long)unit * (pairs + ATTN_TURN) + ATTN_TURN;
-  const int w0 = (int)(start / share), parts = (int)((start + pairs - 1) / share) - w0 + 1;
-  if (parts == 1) return;
+  const int w0 = (int)(start / share), w1 = (int)((start + pairs - 1) / share), parts = w1 - w0 + 1;
+  if (parts == 1 || w1 >= grid) return;  // the latter not while the lengths stay as they were counted
   float m = NEG_INF, l = 0.0f;
   v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int i0 = group; on && i0 < parts; i0 += N * groups) {
@@ -798,7 +799,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, in
     l += f * slot_l[k];
     y += f * sums[k][d];
   }
-  put(y * (l == 0.0f ? 0.0f : 1.0f / l));
+  put(y * (1.0f / l));
 }
 
 // ------------------------------------------------------------------ host

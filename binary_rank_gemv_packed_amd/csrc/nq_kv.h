@@ -96,7 +96,7 @@ __device__ inline float kv_scale(uint32_t top, float most) {
 // division rounds it.  The product with 1 / s is off by under 127.5 x 2^-23 < 2^-16 of it: only
 // within 2^-15 of a tie, and for scales whose reciprocal is not a normal number, does
 // the division itself decide (some 25 instructions; with one for every value 131072
-// tokens of 8 heads took 314 us to write).  A scale of zero (a group below 2^-126) or NaN gives zeros.
+// tokens of 8 heads took 314 us to write).  A scale of zero (a group below 2^-134 x most) or NaN gives zeros.
 // Elsewhere |v / s| is below most + 1/2, for s is within 2^-8 of the quotient it stands for.
 __device__ __forceinline__ void kv_codes(const float (&v)[8], float s, int most, int (&c)[8]) {
   const bool usual = s >= 0x1p-100f && s <= 0x1p100f, some = s > 0.0f;

@@ -227,6 +227,28 @@ def test_queries_that_are_not_finite_stay_in_their_head():
             assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[~hit])
 
 
+@pytest.mark.parametrize("q", [BF, F32])
+@pytest.mark.parametrize("long", [False, True])
+def test_scores_that_are_all_minus_infinity(long, q):
+    """Nothing to weigh is no number, as the formula has it, and not zeros; one finite score
+    takes all the weight."""
+    for kind in KINDS:
+        c = Case([40, 2300 if long else 70], 4, 2, 64, 16, kind, q)
+        first = torch.from_numpy(c.slots).to(DEV)
+        k, v = torch.from_numpy(np.concatenate(c.k)).to(DEV), torch.from_numpy(np.concatenate(c.v)).to(DEV)
+        k[..., 3] = 2.0
+        k[5, 0, 3] = k[45, 1, 3] = 0.0
+        nq.kv_write(k, v, c.cache, first)
+        clean = c.run()
+        c.gq[0, :, 3] = c.gq[1, :, 3] = -3e38  # twice that passes the largest value of fp32
+        y = c.run()
+        assert torch.isfinite(clean).all()
+        assert torch.isnan(y[0, 2:]).all() and torch.isnan(y[1, :2]).all()
+        if kind == "bf16":
+            assert torch.equal(y[0, :2], v[5, 0].bfloat16().to(q).expand(2, -1))
+            assert torch.equal(y[1, 2:], v[45, 1].bfloat16().to(q).expand(2, -1))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("long", [False, True])
 def test_bad_lengths_and_pages_make_their_sequence_nan(kind, long):
