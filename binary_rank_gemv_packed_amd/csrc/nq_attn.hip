@@ -254,16 +254,16 @@ struct Half {
 // lane L channels 8 (L >> 4) .. + 7 of head L & 15.  FINE: three pieces.
 constexpr int query_pieces(bool fine) { return fine ? 3 : 1; }
 
-// A wave's share of them: channels 32 c .. for c = wave, wave + 4.
-template <int D, bool FINE>
+// A wave's share of them: channels 32 c .. for c = wave, wave + WAVES.
+template <int D, bool FINE, int WAVES>
 struct Queries {
-  static constexpr int CH = D / 32, EACH = (CH + ATTN_WAVES - 1) / ATTN_WAVES, PIECES = query_pieces(FINE);
+  static constexpr int CH = D / 32, EACH = (CH + WAVES - 1) / WAVES, PIECES = query_pieces(FINE);
   u32x4_at2 raw[EACH][FINE ? 2 : 1];
   // row: the lane's head, null for none
   __device__ __forceinline__ void load(const void* row, int dtype, int wave, int lane) {
 #pragma unroll
     for (int j = 0; j < EACH; j++) {
-      const int at = 32 * (wave + ATTN_WAVES * j) + 8 * (lane >> 4);
+      const int at = 32 * (wave + WAVES * j) + 8 * (lane >> 4);
 #pragma unroll
       for (int i = 0; i < (FINE ? 2 : 1); i++) raw[j][i] = u32x4_at2{0u, 0u, 0u, 0u};
       if (!row || at >= D) continue;
@@ -278,7 +278,7 @@ struct Queries {
   __device__ __forceinline__ void put(uint32_t (*to)[64][4], int dtype, int wave, int lane) const {
 #pragma unroll
     for (int j = 0; j < EACH; j++) {
-      const int c = wave + ATTN_WAVES * j;
+      const int c = wave + WAVES * j;
       if (c >= CH) continue;
       u32x4 out[PIECES];
 #pragma unroll
@@ -491,11 +491,12 @@ struct Segment {
 
 // Where the tiles of a wave's pairs lie: lane i looks after the wave's pair k + i, k a
 // multiple of 64.  Behind the segment's last pair that one stands again.
+template <int WAVES>
 struct Places {
   int page[2], tile[2];
   int bad;  // (not a bool, whose padding would take the copies through memory)
   __device__ __forceinline__ void look(const AttnArgs& a, const Segment& g, int wave, int lane, int k, int tpp) {
-    int pair = g.p0 + wave + (k + lane) * ATTN_WAVES;
+    int pair = g.p0 + wave + (k + lane) * WAVES;
     pair = g.sp.first_pair() + (pair < g.p1 ? pair : g.p1 - 1);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -528,12 +529,12 @@ struct Places {
 // A wave asks for its next pair's keys as soon as it has the scores of this one's, and for
 // the values when it has added this one's, across the border of two segments too: the
 // next segment's places and queries are looked up while this one is worked on.
-template <int D, int KIND, bool FINE, bool NARROW, bool SPLIT>
-__global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
+template <int D, int KIND, bool FINE, bool NARROW, bool SPLIT, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) attn_kernel(AttnArgs a) {
   constexpr int XT = D / 16;
-  __shared__ float part_o[ATTN_WAVES][XT][64][4];
+  __shared__ float part_o[WAVES][XT][64][4];
   __shared__ uint32_t queries[query_pieces(FINE) * D / 32][64][4];
-  __shared__ float part_m[ATTN_WAVES][16], part_l[ATTN_WAVES][16];
+  __shared__ float part_m[WAVES][16], part_l[WAVES][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15;
   const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio), units = heads * tiles;
   const int tpp = a.cache.page / KV_TILE;
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
       const int cols = ratio - g.unit % tiles * 16 < 16 ? ratio - g.unit % tiles * 16 : 16;
       const size_t at = ((size_t)g.b * a.q_heads + g.unit / tiles * ratio + g.unit % tiles * 16) * D;
       const float y = bad_length(a, n) ? __uint_as_float(0x7fc00000u) : 0.0f;
-      for (int i = threadIdx.x; i < cols * D; i += 64 * ATTN_WAVES) {
+      for (int i = threadIdx.x; i < cols * D; i += 64 * WAVES) {
         if (a.y_dtype == 0) static_cast<float*>(a.y)[at + i] = y;
         else static_cast<uint16_t*>(a.y)[at + i] = f32_to_bf16(y);
       }
@@ -579,8 +580,8 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   }
   Wave<D, KIND, FINE, NARROW> w;
   w.lane = lane;
-  Places at, at_ahead;
-  auto locate = [&](const Segment& s, const Places& p, int k) {  // the wave's pair k
+  Places<WAVES> at, at_ahead;
+  auto locate = [&](const Segment& s, const Places<WAVES>& p, int k) {  // the wave's pair k
     const int head = s.unit / tiles;
     Where to;
 #pragma unroll
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
   };
   auto first_head = [&](const Segment& s) { return s.unit / tiles * ratio + s.unit % tiles * 16; };
   auto columns = [&](const Segment& s) { const int c = ratio - s.unit % tiles * 16; return c < 16 ? c : 16; };
-  Queries<D, FINE> query;
+  Queries<D, FINE, WAVES> query;
   auto ask = [&](const Segment& s) {
     const size_t row = ((size_t)s.b * a.q_heads + first_head(s) + col) * D;
     query.load(col < columns(s) ? static_cast<const uint8_t*>(a.q) + row * (a.q_dtype == 2 ? 2 : 4) : nullptr, a.q_dtype, wave, lane);
@@ -642,9 +643,9 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     const int cols = columns(g);
     const size_t q_row = ((size_t)g.b * a.q_heads + first_head(g) + col) * D;
     w.begin();
-    const int count = g.p1 - g.p0 > wave ? (g.p1 - g.p0 - wave + ATTN_WAVES - 1) / ATTN_WAVES : 0;
+    const int count = g.p1 - g.p0 > wave ? (g.p1 - g.p0 - wave + WAVES - 1) / WAVES : 0;
     for (int k = 0; k < count; k++) {
-      const int first = (g.sp.first_pair() + g.p0 + wave + k * ATTN_WAVES) * ATTN_PAIR;
+      const int first = (g.sp.first_pair() + g.p0 + wave + k * WAVES) * ATTN_PAIR;
       float x[NARROW ? 4 : 8];
       w.scores(keys, queries, c, x);
       // the wave's pair k + 1, or the next segment's first, or (no such) a few lines again: a
@@ -687,21 +688,21 @@ __global__ void __launch_bounds__(64 * ATTN_WAVES, 2) attn_kernel(AttnArgs a) {
     for (int x = 0; x < XT; x++) *reinterpret_cast<v4f*>(part_o[wave][x][lane]) = w.o[x];
     if (more) query.put(queries, a.q_dtype, wave, lane);
     __syncthreads();
-    float m = NEG_INF, f[ATTN_WAVES], l = 0.0f;
+    float m = NEG_INF, f[WAVES], l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < ATTN_WAVES; i++) m = fmaxf(m, part_m[i][col]);
+    for (int i = 0; i < WAVES; i++) m = fmaxf(m, part_m[i][col]);
 #pragma unroll
-    for (int i = 0; i < ATTN_WAVES; i++) {
+    for (int i = 0; i < WAVES; i++) {
       f[i] = part_m[i][col] == m ? 1.0f : __builtin_amdgcn_exp2f(part_m[i][col] - m);
       l += f[i] * part_l[i][col];
     }
     const bool whole = g.p0 == 0 && g.p1 == g.sp.pairs();
     const float inv = whole ? 1.0f / l : 1.0f;  // l is 0 where every score is -infinity: a NaN, as the formula's
     float* place = a.part + ((size_t)blockIdx.x * 2 + (g.p0 == 0)) * slot_floats(D);
-    for (int x = wave; x < XT; x += ATTN_WAVES) {
+    for (int x = wave; x < XT; x += WAVES) {
       v4f s = *reinterpret_cast<const v4f*>(part_o[0][x][lane]) * f[0];
 #pragma unroll
-      for (int i = 1; i < ATTN_WAVES; i++) s += *reinterpret_cast<const v4f*>(part_o[i][x][lane]) * f[i];
+      for (int i = 1; i < WAVES; i++) s += *reinterpret_cast<const v4f*>(part_o[i][x][lane]) * f[i];
       s *= inv;
       if (col < cols) {
         const int ch = 16 * x + 4 * (lane >> 4);
@@ -803,20 +804,46 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, in
 }
 
 // ------------------------------------------------------------------ host
+// Units as they are, a workgroup each, or cut into equal shares and joined?  The former is
+// one launch (the join is some 6 us with its launch) but takes its longest unit's time; the latter takes 11
+// us at least, and more where parts are many.  So the former is for units that take, by
+// what the host knows of the longest, no more than 5.5 us beside what any launch takes, and up to 13
+// where there are many units.  8 key heads of 128, 8 bits, in us as units and cut: 1 x 512 tokens
+// 8.4 and 10.4, 1 x 1024 11.5 and 11.1, 8 x 1024 11.9 and 16.1, 16 x 2048 18.8 and 22.0, 64 of 1
+// to 1536 25.8 and 30.9; beyond the limit 8 of 1 to 2048 17.7 and 16.8, 16 of 1 to 3000 23.8 and 20.7.
+constexpr float attn_unit_ns(int units) { return units < 120 ? 5500.0f + 62.5f * units : 13000.0f; }
+// What a token of a long unit costs, by the chip's times over 1024 to 2048 tokens, heads of 64 to
+// 256: bf16 5.0 to 16.6 ns (60 bytes a ns into a CU), codes with four waves 8.2 to 11.8, as long as an
+// access takes, with eight 5.0 to 10.1; FINE 8 bits 6.3 to 10.1, 15.4 with four waves, 4
+// bits 7.3 to 20, four waves 11 to 26.
+// Eight waves are for codes and as many units as there are CUs (16 x 1024 tokens of 8 bits 14.3 ->
+// 12.3 us, 8 x 1024 of 4 bits 16.8 -> 12.6); for up to 256 tokens (16 x 256: 7.3 -> 7.5 us), bf16 (16 x
+// 1024: 15.7 -> 16.3) and more units (64 x 512 of 8 bits 15.8 -> 16.5) four are faster.
+constexpr float attn_token_ns(int D, int kind, bool fine, bool wide) {
+  if (kind == KV_BF16) return 1.0f + D / 16.5f;
+  if (kind == KV_INT8) return wide ? (3.5f + D / 50.0f) * (fine ? 1.25f : 1.0f) : 7.0f + D / (fine ? 30.0f : 60.0f);
+  return wide ? fine ? D / 10.0f : 3.5f + D / 40.0f : 7.0f + D / (fine ? 13.0f : 60.0f);
+}
+
 template <int D, int KIND, bool FINE, bool NARROW>
 void attn_launch(const AttnArgs& a) {
   const int heads = a.cache.heads, units = heads * head_tiles(a.q_heads / heads);
   constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
-  // Units as they are, a workgroup each, where none is long: no join (some 6 us with its
-  // launch), but a long unit beside short ones is one workgroup's.  8 key heads of 128, 8 bits,
-  // one launch and two: 16 x 1024 tokens 13.8 and 18.2 us, 1 x 1024 12.1 and 10.7, 64 x 2048 48.2
-  // and 54.7, but 64 of 16 to 4096 tokens (spread over the logarithm) 38.7 and 29.3.
   const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
-  if (longest <= 1024) {
-    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false>), dim3((unsigned)(a.B * units)), dim3(64 * ATTN_WAVES), 0, a.stream, a);
+  constexpr bool can_wide = KIND != KV_BF16 && !(FINE && D == 256);  // (those would spill)
+  const bool wide = can_wide && a.B * units <= 256 && longest > 256;
+  if (longest * attn_token_ns(D, KIND, FINE, wide) <= attn_unit_ns(a.B * units)) {
+    const dim3 blocks((unsigned)(a.B * units));
+    if constexpr (can_wide) {
+      if (wide) {
+        hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, 8>), blocks, dim3(512), 0, a.stream, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, ATTN_WAVES>), blocks, dim3(64 * ATTN_WAVES), 0, a.stream, a);
     return;
   }
-  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
+  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
   // Heads of a workgroup of the join: one where there are few, else as many as leave the
   // longest unit (all tokens in one sequence) 64 parts a group at most.  With one head each
   // 64 sequences of 64 heads take 11.9 us instead of 5.8.

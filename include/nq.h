@@ -444,8 +444,9 @@ nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots,
  * bf16 (2^-8) for bf16 q and y, else not.  What lies in slots that are not seen
  * does not matter.  Asynchronous on `stream`, capturable (lengths and table are read by
  * the kernels); calls that overlap in time need workspaces of their own; repeated calls
- * give identical bits.  B == 0 launches nothing.  max_length and the window choose
- * between one launch (up to 1024 tokens) and a split over the length with a join. */
+ * give identical bits.  B == 0 launches nothing.  B, max_length and the window choose
+ * between one launch (up to some 1000 tokens, 2000 in large batches) and a split over the
+ * length with a join. */
 size_t nq_kv_attention_workspace_bytes(const nq_kv_cache* C);
 nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_t q_dtype, int32_t q_heads,
                           const int32_t* table, int32_t table_width, const int32_t* lengths, int32_t max_length,

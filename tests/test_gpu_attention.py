@@ -114,6 +114,22 @@ def test_more_than_eight_query_heads_a_key_head(D, kind, q):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("q", [BF, F32])
+def test_few_and_many_units(D, kind, q):
+    """Some tens of units of a few hundred tokens, and several hundred of them: what a
+    workgroup has to do with a unit depends on both, and on what is known of the lengths."""
+    c = Case([300, 1, 0, 513, 700, 257], 12, 2, D, 32, kind, q)
+    for most in (0, 700, 1000, 4000):
+        c.check(c.run(max_length=most))
+    lengths = [(37 * i) % 301 for i in range(140)]
+    c = Case(lengths, 4, 2, D, 32, kind, q)
+    c.check(c.run(), list(range(0, 140, 9)))
+    c = Case([2000, 1500, 90], 8, 2, D, 32, kind, q, window=400)
+    c.check(c.run())
+
+
 def test_many_sequences():
     """More sequences than a wave has lanes, several times over, most of them empty, in one
     launch and in two."""
