@@ -247,7 +247,9 @@ def test_queries_that_are_not_finite_stay_in_their_head():
 @pytest.mark.parametrize("long", [False, True])
 def test_scores_that_are_all_minus_infinity(long, q):
     """Nothing to weigh is no number, as the formula has it, and not zeros; one finite score
-    takes all the weight."""
+    takes all the weight.  Products with 2 of q's -3e38 pass the largest value of fp32, and with
+    127 of 8 bits; 4 bits take 7 / 16 of it for fp32 q (-1.3e38, and the scores times
+    scale stay finite): the formula's values, tied tokens alike."""
     for kind in KINDS:
         c = Case([40, 2300 if long else 70], 4, 2, 64, 16, kind, q)
         first = torch.from_numpy(c.slots).to(DEV)
@@ -256,9 +258,16 @@ def test_scores_that_are_all_minus_infinity(long, q):
         k[5, 0, 3] = k[45, 1, 3] = 0.0
         nq.kv_write(k, v, c.cache, first)
         clean = c.run()
-        c.gq[0, :, 3] = c.gq[1, :, 3] = -3e38  # twice that passes the largest value of fp32
+        c.gq[0, :, 3] = c.gq[1, :, 3] = -3e38
         y = c.run()
         assert torch.isfinite(clean).all()
+        if kind == "int4" and q == F32:
+            for b, at in ((0, slice(0, 40)), (1, slice(40, None))):
+                held = [O.held(t[at].cpu().numpy(), kind) for t in (k, v)]
+                want, mag, _ = O.attention(c.gq[b].double().cpu().numpy(), *held, 64 ** -0.5)
+                # equal weights of one: n sums, their quotient and the scales' products, 2^-24 each
+                assert np.all(np.abs(y[b].double().cpu().numpy() - want) <= (c.lengths[b] / 32 + 72) * E * mag)
+            continue
         assert torch.isnan(y[0, 2:]).all() and torch.isnan(y[1, :2]).all()
         if kind == "bf16":
             assert torch.equal(y[0, :2], v[5, 0].bfloat16().to(q).expand(2, -1))
