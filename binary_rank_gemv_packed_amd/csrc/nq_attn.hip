@@ -46,7 +46,6 @@ typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int ATTN_WAVES = 4;
-constexpr int ATTN_GRID_MAX = 768;
 // Workgroups that share the tokens of all sequences: as many as a chip of 256 CUs holds at
 // once.  Three a CU for bf16 results of 4-bit caches (up to eight query heads a key head),
 // whose registers allow it and whose vector and matrix instructions it overlaps (131072 tokens
@@ -54,6 +53,11 @@ constexpr int ATTN_GRID_MAX = 768;
 constexpr int attn_grid(int D, int kind, bool fine, bool narrow) {
   return kind == KV_INT4 && !fine && narrow && D <= 128 ? 768 : 512;
 }
+// Whether more than 16 query heads a key head go 32 at a time, so that the cache is read once for
+// them: 64 sequences of 4096 tokens, 32 heads of one key head, bf16 55.7 -> 40.7 us, 8 bits 37.7 ->
+// 32.2.  Not 4 bits, which wait for their vector instructions (35.8 and 35.3 us), nor FINE or more
+// channels, which have no registers or shared memory for it.
+constexpr bool attn_two(int D, int kind, bool fine) { return D <= 128 && kind != KV_INT4 && !fine; }
 constexpr int ATTN_PAIR = 32;     // tokens of a wave's step: two tiles
 // What a unit costs beside its pairs (its queries, places and the waves' join), in pairs:
 // 64 sequences of 256 to 4096 tokens of 8 bits 57.0 us counted as 0, 49.8 as 4, 46.9 as 8, 47.5 as 12.
@@ -159,8 +163,10 @@ __device__ __forceinline__ long long share_of(long long total, int grid) {
   return even < ATTN_WAVES ? ATTN_WAVES : even;
 }
 
-__host__ __device__ inline int head_tiles(int ratio) { return (ratio + 15) / 16; }
-__host__ __device__ inline size_t slot_floats(int D) { return 16 * D + 32; }
+// Units of a key head's query heads, `cols` (16 or 32) each, and a part of one in the
+// workspace: sums [cols][D], maxima [cols], weights' sums [cols].
+__host__ __device__ inline int head_tiles(int ratio, int cols) { return (ratio + cols - 1) / cols; }
+__host__ __device__ inline size_t slot_floats(int D, int cols) { return (size_t)cols * (D + 2); }
 
 // ------------------------------------------------------------------ a wave's step
 // Codes are read once, past the caches: 131072 tokens of 8 bits 61.0 -> 55.5 us, of bf16
@@ -254,23 +260,25 @@ struct Half {
   }
 };
 
-// Queries as the operand of the MFMA, in shared memory: [piece][32 channels][64 lanes],
+// Queries as the operand of the MFMA, in shared memory: [piece][16 heads][32 channels][64 lanes],
 // lane L channels 8 (L >> 4) .. + 7 of head L & 15.  FINE: three pieces.
 constexpr int query_pieces(bool fine) { return fine ? 3 : 1; }
 
-// A wave's share of them: channels 32 c .. for c = wave, wave + WAVES.
-template <int D, bool FINE, int WAVES>
+// A wave's share of them: channels 32 c .. of 16 heads for c = wave, wave + WAVES (and, with HT =
+// 2, of the next 16 for c behind D / 32).
+template <int D, bool FINE, int WAVES, int HT>
 struct Queries {
-  static constexpr int CH = D / 32, EACH = (CH + WAVES - 1) / WAVES, PIECES = query_pieces(FINE);
+  static constexpr int CH = D / 32, ALL = HT * CH, EACH = (ALL + WAVES - 1) / WAVES, PIECES = query_pieces(FINE);
   u32x4_at2 raw[EACH][FINE ? 2 : 1];
-  // row: the lane's head, null for none
-  __device__ __forceinline__ void load(const void* row, int dtype, int wave, int lane) {
+  // row: the lane's head of the first 16, null for none; next: whether it has one of the next 16
+  __device__ __forceinline__ void load(const void* row, bool next, int dtype, int wave, int lane) {
 #pragma unroll
     for (int j = 0; j < EACH; j++) {
-      const int at = 32 * (wave + WAVES * j) + 8 * (lane >> 4);
+      const int c = wave + WAVES * j, h = HT == 1 ? 0 : c / CH;
+      const int at = 32 * (HT == 1 ? c : c % CH) + 8 * (lane >> 4) + h * 16 * D;
 #pragma unroll
       for (int i = 0; i < (FINE ? 2 : 1); i++) raw[j][i] = u32x4_at2{0u, 0u, 0u, 0u};
-      if (!row || at >= D) continue;
+      if (!row || c >= ALL || (h && !next)) continue;
       if (FINE && dtype == 0) {
 #pragma unroll
         for (int i = 0; i < (FINE ? 2 : 1); i++) raw[j][i] = reinterpret_cast<const u32x4_at2*>(static_cast<const float*>(row) + at)[i];
@@ -283,7 +291,7 @@ struct Queries {
 #pragma unroll
     for (int j = 0; j < EACH; j++) {
       const int c = wave + WAVES * j;
-      if (c >= CH) continue;
+      if (c >= ALL) continue;
       u32x4 out[PIECES];
 #pragma unroll
       for (int p = 0; p < PIECES; p++) out[p] = u32x4{0u, 0u, 0u, 0u};
@@ -309,7 +317,7 @@ struct Queries {
         out[0] = raw[j][0];
       }
 #pragma unroll
-      for (int p = 0; p < PIECES; p++) *reinterpret_cast<u32x4*>(to[p * CH + c][lane]) = out[p];
+      for (int p = 0; p < PIECES; p++) *reinterpret_cast<u32x4*>(to[p * ALL + c][lane]) = out[p];
     }
   }
 };
@@ -323,62 +331,75 @@ __device__ __forceinline__ uint32_t eight_on(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x108, 0xf, 0xf, true);
 }
 
-template <int D, int KIND, bool FINE, bool NARROW>
+template <int D, int KIND, bool FINE, bool NARROW, int HT>
 struct Wave {
   static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE);
   static constexpr int TILES = NARROW ? 1 : 2, X = 4 * TILES;  // scores of a lane
   static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24
-  v4f o[XT];
-  float m, safe, l;
+  v4f o[HT][XT];
+  float m[HT], safe[HT], l[HT];
   int lane;
   Nibbles nb;
 
   __device__ __forceinline__ void begin() {
-    m = NEG_INF;
-    safe = l = 0.0f;
 #pragma unroll
-    for (int x = 0; x < XT; x++) o[x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < HT; t++) {
+      m[t] = NEG_INF;
+      safe[t] = l[t] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < XT; x++) o[t][x] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
   }
 
-  // the scores (in powers of two) of the lane's 2 x 4 tokens (NARROW: 4) of its head
-  __device__ __forceinline__ void scores(const Half<D, KIND, false, NARROW>& t, const uint32_t (*q)[64][4], float c, float (&x)[X]) const {
+  // the scores (in powers of two) of the lane's 2 x 4 tokens (NARROW: 4) of its head (HT = 2:
+  // and of the sixteenth behind it)
+  __device__ __forceinline__ void scores(const Half<D, KIND, false, NARROW>& t, const uint32_t (*q)[64][4], float c,
+                                         float (&x)[HT][X]) const {
     const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
-    v4f s[2];
-    s[0] = s[1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    v4f s[HT][2];
+#pragma unroll
+    for (int h = 0; h < HT; h++) s[h][0] = s[h][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int ch = 0; ch < CH; ch++) {
-      u32x4 query[PIECES];
+      u32x4 key[2];
 #pragma unroll
-      for (int p = 0; p < PIECES; p++) query[p] = *reinterpret_cast<const u32x4*>(q[p * CH + ch][lane]);
-      v4f less = {0.0f, 0.0f, 0.0f, 0.0f}, d[2];
-      if constexpr (BIAS) less = mfma(minus, query[0], less);
+      for (int h = 0; h < HT; h++) {
+        u32x4 query[PIECES];
 #pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const u32x4 key = t.template keys<FINE>(i, ch, nb);
-        d[i] = KIND == KV_INT4 ? less : s[i];
+        for (int p = 0; p < PIECES; p++) query[p] = *reinterpret_cast<const u32x4*>(q[(p * HT + h) * CH + ch][lane]);
+        v4f less = {0.0f, 0.0f, 0.0f, 0.0f}, d[2];
+        if constexpr (BIAS) less = mfma(minus, query[0], less);
 #pragma unroll
-        for (int p = PIECES - 1; p >= 0; p--) d[i] = mfma(key, query[p], d[i]);
-        if constexpr (KIND != KV_INT4) s[i] = d[i];
-      }
-      if constexpr (KIND == KV_INT4) {
+        for (int i = 0; i < 2; i++) {
+          if (h == 0) key[i] = t.template keys<FINE>(i, ch, nb);
+          d[i] = KIND == KV_INT4 ? less : s[h][i];
 #pragma unroll
-        for (int i = 0; i < TILES; i++)
+          for (int p = PIECES - 1; p >= 0; p--) d[i] = mfma(key[i], query[p], d[i]);
+          if constexpr (KIND != KV_INT4) s[h][i] = d[i];
+        }
+        if constexpr (KIND == KV_INT4) {
 #pragma unroll
-          for (int j = 0; j < 4; j++) s[i][j] = fmaf(t.scale(i, ch, j), NARROW ? two_tiles(d[0][j], d[1][j]) : d[i][j], s[i][j]);
+          for (int i = 0; i < TILES; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+              s[h][i][j] = fmaf(t.scale(i, ch, j), NARROW ? two_tiles(d[0][j], d[1][j]) : d[i][j], s[h][i][j]);
+        }
       }
     }
 #pragma unroll
-    for (int j = 0; j < X; j++) {
-      x[j] = s[j / 4][j & 3];
-      if constexpr (NARROW && KIND != KV_INT4) x[j] = two_tiles(s[0][j], s[1][j]);
-      x[j] *= KIND == KV_INT8 ? c * t.scale(j / 4, 0, j & 3) : c;
-    }
+    for (int h = 0; h < HT; h++)
+#pragma unroll
+      for (int j = 0; j < X; j++) {
+        x[h][j] = s[h][j / 4][j & 3];
+        if constexpr (NARROW && KIND != KV_INT4) x[h][j] = two_tiles(s[h][0][j], s[h][1][j]);
+        x[h][j] *= KIND == KV_INT8 ? c * t.scale(j / 4, 0, j & 3) : c;
+      }
   }
 
   // Scores to weights.  32 tokens from `first` on, of which those from lo to n - 1 are seen:
   // the others weigh nothing and `keep` masks their values (bf16) or scales, for what
   // lies there may be anything.
-  __device__ __forceinline__ void weigh(float (&x)[X], int first, int lo, int n, uint32_t (&keep)[4]) {
+  __device__ __forceinline__ void weigh(float (&x)[HT][X], int first, int lo, int n, uint32_t (&keep)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; i++) keep[i] = ~0u;
     if (first < lo || first + ATTN_PAIR > n) {
@@ -387,7 +408,9 @@ struct Wave {
 #pragma unroll
       for (int j = 0; j < X; j++) {
         const int token = at + (NARROW ? 2 * (lane & 8) : j / 4 * 16) + (j & 3);
-        if (token < lo || token >= n) x[j] = NEG_INF;
+#pragma unroll
+        for (int h = 0; h < HT; h++)
+          if (token < lo || token >= n) x[h][j] = NEG_INF;
       }
       // bf16 values of both tiles; scales of the lane's own
 #pragma unroll
@@ -396,51 +419,51 @@ struct Wave {
         if (token < lo || token >= n) keep[j / 2] &= j & 1 ? 0xffffu : 0xffff0000u;
       }
     }
-    float top = NEG_INF;
 #pragma unroll
-    for (int j = 0; j < X; j++) top = fmaxf(top, x[j]);
-    if (__any(top > m + ATTN_RISE)) raise(top);
+    for (int h = 0; h < HT; h++) {
+      float top = NEG_INF;
 #pragma unroll
-    for (int j = 0; j < X; j++) x[j] = __builtin_amdgcn_exp2f(x[j] - safe);
+      for (int j = 0; j < X; j++) top = fmaxf(top, x[h][j]);
+      if (__any(top > m[h] + ATTN_RISE)) raise(h, top);
+#pragma unroll
+      for (int j = 0; j < X; j++) x[h][j] = __builtin_amdgcn_exp2f(x[h][j] - safe[h]);
+    }
   }
 
-  __device__ __forceinline__ void add(Half<D, KIND, true, NARROW>& t, const float (&p)[X], const uint32_t (&keep)[4], bool edge) {
-    if constexpr (NG == 0) {
-      u32x4 w[PIECES];
-      weights(p, w);
+  __device__ __forceinline__ void add(Half<D, KIND, true, NARROW>& t, const float (&p)[HT][X], const uint32_t (&keep)[4], bool edge) {
+    if (NG && edge) {
+      asm volatile("");
 #pragma unroll
-      for (int j = 0; j < X / 2; j++) l += FINE ? p[2 * j] + p[2 * j + 1] : low_f32(w[0][j]) + high_f32(w[0][j]);
+      for (int i = 0; i < TILES; i++)
 #pragma unroll
-      for (int x = 0; x < XT; x++) {
-        const u32x4 value = t.template values<FINE>(x, keep, nb);
+        for (int k = 0; k < 2 * NG; k++) t.s[i][k] &= keep[2 * i + (k & 1)];
+    }
+    constexpr int GROUPS = NG ? NG : 1;
 #pragma unroll
-        for (int i = PIECES - 1; i >= 0; i--) o[x] = mfma(value, w[i], o[x]);
-      }
-    } else {
-      if (edge) {
-        asm volatile("");
+    for (int g = 0; g < GROUPS; g++) {
+      u32x4 w[HT][PIECES];
 #pragma unroll
-        for (int i = 0; i < TILES; i++)
-#pragma unroll
-          for (int k = 0; k < 2 * NG; k++) t.s[i][k] &= keep[2 * i + (k & 1)];
-      }
-#pragma unroll
-      for (int j = 0; j < X; j++) l += p[j];
-#pragma unroll
-      for (int g = 0; g < NG; g++) {
+      for (int h = 0; h < HT; h++) {
         float ps[X];
 #pragma unroll
-        for (int j = 0; j < X; j++) ps[j] = p[j] * t.scale(j / 4, g, j & 3);
-        u32x4 w[PIECES];
-        weights(ps, w);
+        for (int j = 0; j < X; j++) ps[j] = NG ? p[h][j] * t.scale(j / 4, NG ? g : 0, j & 3) : p[h][j];
+        weights(ps, w[h]);
+        if (g == 0) {
 #pragma unroll
-        for (int x = g * XT / NG; x < (g + 1) * XT / NG; x++) {
-          const u32x4 value = t.template values<FINE>(x, keep, nb);
+          for (int j = 0; j < X / 2; j++)
+            l[h] += NG || FINE ? p[h][2 * j] + p[h][2 * j + 1] : low_f32(w[h][0][j]) + high_f32(w[h][0][j]);
+        }
+      }
 #pragma unroll
-          for (int i = PIECES - 1; i >= 0; i--) o[x] = mfma(value, w[i], o[x]);
+      for (int x = g * XT / GROUPS; x < (g + 1) * XT / GROUPS; x++) {
+        const u32x4 value = t.template values<FINE>(x, keep, nb);
+#pragma unroll
+        for (int h = 0; h < HT; h++) {
+#pragma unroll
+          for (int i = PIECES - 1; i >= 0; i--) o[h][x] = mfma(value, w[h][i], o[h][x]);
           if constexpr (BIAS) {
             const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
-            o[x] = mfma(minus, w[0], o[x]);
+            o[h][x] = mfma(minus, w[h][0], o[h][x]);
           }
         }
       }
@@ -462,17 +485,17 @@ struct Wave {
     }
   }
 
-  __device__ __forceinline__ void raise(float top) {
+  __device__ __forceinline__ void raise(int h, float top) {
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     if constexpr (NARROW) top = fmaxf(top, __shfl_xor(top, 8));
-    const float to = fmaxf(m, top);
-    const float f = to == m ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-    m = to;
-    safe = to == NEG_INF ? 0.0f : to;
-    l *= f;
+    const float to = fmaxf(m[h], top);
+    const float f = to == m[h] ? 1.0f : __builtin_amdgcn_exp2f(m[h] - to);
+    m[h] = to;
+    safe[h] = to == NEG_INF ? 0.0f : to;
+    l[h] *= f;
 #pragma unroll
-    for (int x = 0; x < XT; x++) o[x] *= f;
+    for (int x = 0; x < XT; x++) o[h][x] *= f;
   }
 };
 
@@ -533,14 +556,14 @@ struct Places {
 // A wave asks for its next pair's keys as soon as it has the scores of this one's, and for
 // the values when it has added this one's, across the border of two segments too: the
 // next segment's places and queries are looked up while this one is worked on.
-template <int D, int KIND, bool FINE, bool NARROW, bool SPLIT, int WAVES>
+template <int D, int KIND, bool FINE, bool NARROW, bool SPLIT, int WAVES, int HT>
 __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) attn_kernel(AttnArgs a) {
-  constexpr int XT = D / 16;
-  __shared__ float part_o[WAVES][XT][64][4];
-  __shared__ uint32_t queries[query_pieces(FINE) * D / 32][64][4];
-  __shared__ float part_m[WAVES][16], part_l[WAVES][16];
+  constexpr int XT = D / 16, COLS = 16 * HT;
+  __shared__ float part_o[WAVES][HT * XT][64][4];
+  __shared__ uint32_t queries[query_pieces(FINE) * HT * D / 32][64][4];
+  __shared__ float part_m[WAVES][COLS], part_l[WAVES][COLS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15;
-  const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio), units = heads * tiles;
+  const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio, COLS), units = heads * tiles;
   const int tpp = a.cache.page / KV_TILE;
   constexpr float CODES = KIND == KV_INT4 && FINE ? 16.0f : 1.0f;  // what codes_bf16() leaves out
   const float c = a.scale * 1.44269504088896341f * CODES;
@@ -573,8 +596,8 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
     left = 0;
     g.at(span_of(a, n), blockIdx.x / units, blockIdx.x % units, 0, (long long)1 << 40);
     if (g.empty()) {
-      const int cols = ratio - g.unit % tiles * 16 < 16 ? ratio - g.unit % tiles * 16 : 16;
-      const size_t at = ((size_t)g.b * a.q_heads + g.unit / tiles * ratio + g.unit % tiles * 16) * D;
+      const int cols = ratio - g.unit % tiles * COLS < COLS ? ratio - g.unit % tiles * COLS : COLS;
+      const size_t at = ((size_t)g.b * a.q_heads + g.unit / tiles * ratio + g.unit % tiles * COLS) * D;
       const float y = bad_length(a, n) ? __uint_as_float(0x7fc00000u) : 0.0f;
       for (int i = threadIdx.x; i < cols * D; i += 64 * WAVES) {
         if (a.y_dtype == 0) static_cast<float*>(a.y)[at + i] = y;
@@ -583,7 +606,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
       return;
     }
   }
-  Wave<D, KIND, FINE, NARROW> w;
+  Wave<D, KIND, FINE, NARROW, HT> w;
   w.lane = lane;
   Places<WAVES> at, at_ahead;
   auto locate = [&](const Segment& s, const Places<WAVES>& p, int k) {  // the wave's pair k
@@ -598,12 +621,13 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
     }
     return to;
   };
-  auto first_head = [&](const Segment& s) { return s.unit / tiles * ratio + s.unit % tiles * 16; };
-  auto columns = [&](const Segment& s) { const int c = ratio - s.unit % tiles * 16; return c < 16 ? c : 16; };
-  Queries<D, FINE, WAVES> query;
+  auto first_head = [&](const Segment& s) { return s.unit / tiles * ratio + s.unit % tiles * COLS; };
+  auto columns = [&](const Segment& s) { const int c = ratio - s.unit % tiles * COLS; return c < COLS ? c : COLS; };
+  Queries<D, FINE, WAVES, HT> query;
   auto ask = [&](const Segment& s) {
     const size_t row = ((size_t)s.b * a.q_heads + first_head(s) + col) * D;
-    query.load(col < columns(s) ? static_cast<const uint8_t*>(a.q) + row * (a.q_dtype == 2 ? 2 : 4) : nullptr, a.q_dtype, wave, lane);
+    query.load(col < columns(s) ? static_cast<const uint8_t*>(a.q) + row * (a.q_dtype == 2 ? 2 : 4) : nullptr,
+               16 + col < columns(s), a.q_dtype, wave, lane);
   };
   Half<D, KIND, false, NARROW> keys;
   Half<D, KIND, true, NARROW> values;
@@ -651,7 +675,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
     const int count = g.p1 - g.p0 > wave ? (g.p1 - g.p0 - wave + WAVES - 1) / WAVES : 0;
     for (int k = 0; k < count; k++) {
       const int first = (g.sp.first_pair() + g.p0 + wave + k * WAVES) * ATTN_PAIR;
-      float x[NARROW ? 4 : 8];
+      float x[HT][NARROW ? 4 : 8];
       w.scores(keys, queries, c, x);
       // the wave's pair k + 1, or the next segment's first, or (no such) a few lines again: a
       // load that may be left out would make the compiler wait for all of them
@@ -679,46 +703,56 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
       keys.load(next, lane);
       values.load(next, lane);
     }
-    w.l += __shfl_xor(w.l, 16);
-    w.l += __shfl_xor(w.l, 32);
-    if constexpr (NARROW) w.l += __shfl_xor(w.l, 8);
-    if (__any(at.bad)) w.l = __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int h = 0; h < HT; h++) {
+      w.l[h] += __shfl_xor(w.l[h], 16);
+      w.l[h] += __shfl_xor(w.l[h], 32);
+      if constexpr (NARROW) w.l[h] += __shfl_xor(w.l[h], 8);
+      if (__any(at.bad)) w.l[h] = __uint_as_float(0x7fc00000u);
+    }
     // the waves' sums: every wave adds a share of the channels, in the order of the waves
     __syncthreads();
-    if (lane < 16) {
-      part_m[wave][lane] = w.m;
-      part_l[wave][lane] = w.l;
-    }
 #pragma unroll
-    for (int x = 0; x < XT; x++) *reinterpret_cast<v4f*>(part_o[wave][x][lane]) = w.o[x];
+    for (int h = 0; h < HT; h++) {
+      if (lane < 16) {
+        part_m[wave][16 * h + lane] = w.m[h];
+        part_l[wave][16 * h + lane] = w.l[h];
+      }
+#pragma unroll
+      for (int x = 0; x < XT; x++) *reinterpret_cast<v4f*>(part_o[wave][h * XT + x][lane]) = w.o[h][x];
+    }
     if (more) query.put(queries, a.q_dtype, wave, lane);
     __syncthreads();
-    float m = NEG_INF, f[WAVES], l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < WAVES; i++) m = fmaxf(m, part_m[i][col]);
+    for (int h = 0; h < HT; h++) {
+      const int head = 16 * h + col;
+      float m = NEG_INF, f[WAVES], l = 0.0f;
 #pragma unroll
-    for (int i = 0; i < WAVES; i++) {
-      f[i] = part_m[i][col] == m ? 1.0f : __builtin_amdgcn_exp2f(part_m[i][col] - m);
-      l += f[i] * part_l[i][col];
-    }
-    const bool whole = g.p0 == 0 && g.p1 == g.sp.pairs();
-    const float inv = (whole ? 1.0f / l : 1.0f) * CODES;  // l is 0 where every score is -infinity: a NaN, as the formula's
-    float* place = a.part + ((size_t)blockIdx.x * 2 + (g.p0 == 0)) * slot_floats(D);
-    for (int x = wave; x < XT; x += WAVES) {
-      v4f s = *reinterpret_cast<const v4f*>(part_o[0][x][lane]) * f[0];
+      for (int i = 0; i < WAVES; i++) m = fmaxf(m, part_m[i][head]);
 #pragma unroll
-      for (int i = 1; i < WAVES; i++) s += *reinterpret_cast<const v4f*>(part_o[i][x][lane]) * f[i];
-      s *= inv;
-      if (col < cols) {
-        const int ch = 16 * x + 4 * (lane >> 4);
-        if (!whole) *reinterpret_cast<v4f*>(place + col * D + ch) = s;
-        else if (a.y_dtype == 0) *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + q_row + ch) = s;
-        else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + q_row + ch) = u32x2{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+      for (int i = 0; i < WAVES; i++) {
+        f[i] = part_m[i][head] == m ? 1.0f : __builtin_amdgcn_exp2f(part_m[i][head] - m);
+        l += f[i] * part_l[i][head];
       }
-    }
-    if (!whole && wave == 0 && lane < 16) {
-      place[16 * D + lane] = m;
-      place[16 * D + 16 + lane] = l;
+      const bool whole = g.p0 == 0 && g.p1 == g.sp.pairs();
+      const float inv = (whole ? 1.0f / l : 1.0f) * CODES;  // l is 0 where every score is -infinity: a NaN, as the formula's
+      float* place = a.part + ((size_t)blockIdx.x * 2 + (g.p0 == 0)) * slot_floats(D, COLS);
+      for (int x = wave; x < XT; x += WAVES) {
+        v4f s = *reinterpret_cast<const v4f*>(part_o[0][h * XT + x][lane]) * f[0];
+#pragma unroll
+        for (int i = 1; i < WAVES; i++) s += *reinterpret_cast<const v4f*>(part_o[i][h * XT + x][lane]) * f[i];
+        s *= inv;
+        if (head < cols) {
+          const int ch = 16 * x + 4 * (lane >> 4);
+          if (!whole) *reinterpret_cast<v4f*>(place + head * D + ch) = s;
+          else if (a.y_dtype == 0) *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + q_row + 16 * h * D + ch) = s;
+          else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + q_row + 16 * h * D + ch) = u32x2{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+        }
+      }
+      if (!whole && wave == 0 && lane < 16) {
+        place[COLS * D + 16 * h + lane] = m;
+        place[COLS * (D + 1) + 16 * h + lane] = l;
+      }
     }
     if (!more) return;
     g = ahead;
@@ -730,18 +764,18 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
 // D / 4 threads go through the parts of a head that fall to their group of them, eight
 // parts in flight, and the groups' sums are added in order.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, int hb, int blocks) {
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, int cols, int hb, int blocks) {
   constexpr int Q = D / 4, SLOTS = 256 / Q, N = 8;
   __shared__ v4f sums[SLOTS][Q];
   __shared__ float slot_m[SLOTS], slot_l[SLOTS];
-  const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio), units = heads * tiles;
+  const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio, cols), units = heads * tiles;
   const int b = blockIdx.y, unit = blockIdx.x / blocks, tid = threadIdx.x;
   Lengths lengths;
   const Counts n(a, lengths);
   const int length = n.each > 1 ? a.lengths[b] : __builtin_amdgcn_readlane(lengths.held, b), pairs = span_of(a, length).pairs();
   const int slot = tid / Q, d = tid % Q, groups = SLOTS / hb, group = slot / hb, col = blockIdx.x % blocks * hb + slot % hb;
-  const bool on = group < groups && col < 16 && unit % tiles * 16 + col < ratio;
-  const size_t at = ((size_t)b * a.q_heads + unit / tiles * ratio + unit % tiles * 16 + col) * D + 4 * d;
+  const bool on = group < groups && col < cols && unit % tiles * cols + col < ratio;
+  const size_t at = ((size_t)b * a.q_heads + unit / tiles * ratio + unit % tiles * cols + col) * D + 4 * d;
   auto put = [&](v4f y) {
     if (a.y_dtype == 0) *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = y;
     else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
@@ -765,9 +799,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, in
 #pragma unroll
     for (int k = 0; k < N; k++) {  // behind the last part this group's first stands again, with no weight
       const int i = i0 + k * groups < parts ? i0 + k * groups : i0;
-      const float* p = a.part + ((size_t)(w0 + i) * 2 + (i == 0)) * slot_floats(D);
-      pm[k] = p[16 * D + col];
-      pl[k] = p[16 * D + 16 + col];
+      const float* p = a.part + ((size_t)(w0 + i) * 2 + (i == 0)) * slot_floats(D, cols);
+      pm[k] = p[cols * D + col];
+      pl[k] = p[cols * (D + 1) + col];
       py[k] = *reinterpret_cast<const v4f*>(p + col * D + 4 * d);
     }
     float to = m;
@@ -830,10 +864,25 @@ constexpr float attn_token_ns(int D, int kind, bool fine, bool wide) {
   return wide ? fine ? D / 10.0f : 3.5f + D / 40.0f : 7.0f + D / (fine ? 13.0f : 60.0f);
 }
 
+template <int D, int KIND, bool FINE, bool NARROW, int HT>
+void attn_cut(const AttnArgs& a) {
+  const int ratio = a.q_heads / a.cache.heads, units = a.cache.heads * head_tiles(ratio, 16 * HT);
+  constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
+  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES, HT>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
+  // Heads of a workgroup of the join: one where there are few, else as many as leave the
+  // longest unit (all tokens in one sequence) 64 parts a group at most.  With one head each
+  // 64 sequences of 64 heads take 11.9 us instead of 5.8.
+  constexpr int SLOTS = 256 / (D / 4);
+  const int most = ratio < 16 * HT ? ratio : 16 * HT, groups = (grid / units + 2 + 63) / 64;
+  int hb = a.B * a.q_heads <= 512 || groups >= SLOTS ? 1 : SLOTS / groups;
+  hb = hb < most ? hb : most;
+  const int blocks = (most + hb - 1) / hb;
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, 16 * HT, hb, blocks);
+}
+
 template <int D, int KIND, bool FINE, bool NARROW>
 void attn_launch(const AttnArgs& a) {
-  const int heads = a.cache.heads, units = heads * head_tiles(a.q_heads / heads);
-  constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
+  const int ratio = a.q_heads / a.cache.heads, units = a.cache.heads * head_tiles(ratio, 16);
   const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
   constexpr bool can_wide = KIND != KV_BF16 && !(FINE && D == 256);  // (those would spill)
   const bool wide = can_wide && a.B * units <= 256 && longest > 256;
@@ -841,23 +890,17 @@ void attn_launch(const AttnArgs& a) {
     const dim3 blocks((unsigned)(a.B * units));
     if constexpr (can_wide) {
       if (wide) {
-        hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, 8>), blocks, dim3(512), 0, a.stream, a);
+        hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, 8, 1>), blocks, dim3(512), 0, a.stream, a);
         return;
       }
     }
-    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, ATTN_WAVES>), blocks, dim3(64 * ATTN_WAVES), 0, a.stream, a);
+    hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, false, ATTN_WAVES, 1>), blocks, dim3(64 * ATTN_WAVES), 0, a.stream, a);
     return;
   }
-  hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
-  // Heads of a workgroup of the join: one where there are few, else as many as leave the
-  // longest unit (all tokens in one sequence) 64 parts a group at most.  With one head each
-  // 64 sequences of 64 heads take 11.9 us instead of 5.8.
-  constexpr int SLOTS = 256 / (D / 4);
-  const int ratio = a.q_heads / heads, most = ratio < 16 ? ratio : 16, groups = (grid / units + 2 + 63) / 64;
-  int hb = a.B * a.q_heads <= 512 || groups >= SLOTS ? 1 : SLOTS / groups;
-  hb = hb < most ? hb : most;
-  const int blocks = (most + hb - 1) / hb;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, hb, blocks);
+  if constexpr (attn_two(D, KIND, FINE)) {
+    if (ratio > 16) return attn_cut<D, KIND, FINE, NARROW, 2>(a);
+  }
+  attn_cut<D, KIND, FINE, NARROW, 1>(a);
 }
 
 template <int D>
@@ -871,7 +914,11 @@ void attn_by_kind(const AttnArgs& a) {
 
 }  // namespace
 
-size_t attn_workspace(const KvLayout& l) { return align_up(ATTN_GRID_MAX * 2 * slot_floats(l.D) * 4, 256); }
+size_t attn_workspace(const KvLayout& l) {
+  const size_t one = attn_grid(l.D, l.kind, false, true) * slot_floats(l.D, 16);
+  const size_t two = attn_grid(l.D, l.kind, false, false) * slot_floats(l.D, 32);
+  return align_up((attn_two(l.D, l.kind, false) ? two : one) * 2 * 4, 256);
+}
 
 hipError_t attn_forward(const AttnArgs& a) {
   switch (a.cache.D) {

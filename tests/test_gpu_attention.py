@@ -114,6 +114,18 @@ def test_more_than_eight_query_heads_a_key_head(D, kind, q):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 96, 128, 192])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,H", [(17, 1), (64, 2), (99, 3)])
+def test_more_than_sixteen_query_heads_a_key_head(D, kind, Hq, H):
+    """Some of them 32 at a time: one more than 16, all of 32, one in a second unit; a
+    sequence without tokens, cut units and whole ones, a window."""
+    c = Case([2600, 0, 40, 1, 700, 33], Hq, H, D, 48, kind, BF)
+    c.check(c.run())
+    c = Case([1900, 3000], Hq, H, D, 16, kind, BF, window=1700)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("D", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("q", [BF, F32])
