@@ -24,14 +24,16 @@ namespace nq {
 
 namespace {
 
+typedef uint32_t u32x1_at2 __attribute__((ext_vector_type(1), aligned(2)));
 typedef uint32_t u32x2_at2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 // ------------------------------------------------------------------ lanes
 // LG lanes hold one head's D channels as pairs: lane m the pairs VEC m .. VEC m +
-// VEC - 1, and with C chunks also those LG VEC further on.  VEC = 4 where 8 divides D
-// and R, so that a lane's pairs are all turned or none, and are two runs of four
-// channels; VEC = 1 elsewhere.
+// VEC - 1, and with C chunks also those LG VEC further on.  VEC = 4 or 2 where 2 VEC
+// divides D and R (R only where members of a pair are R / 2 apart), so that a lane's pairs are two
+// runs of VEC channels; VEC = 1 elsewhere: 2048 tokens of 64 + 8 heads of 100 in bf16 21.6 us
+// with 2 and 33.8 with 1 (backward 29.3 and 43.8), of 96 15.9 with 4.
 template <int VEC, int LG, int C>
 struct HeadLanes {
   static constexpr int N = VEC * C;  // pairs of a lane
@@ -46,11 +48,12 @@ struct HeadLanes {
   __device__ __forceinline__ int second(int i) const { return near || !turned(i) ? 2 * pair(i) + 1 : pair(i) + half; }
 };
 
-// Four elements, and a lane's pairs of one head as they are stored, until get(): what
+// VEC elements, and a lane's pairs of one head as they are stored, until get(): what
 // is asked for early takes no more registers than its bytes.
-template <typename T>
-struct Four {
-  typedef typename std::conditional<sizeof(T) == 4, u32x4_at2, u32x2_at2>::type word;
+template <typename T, int VEC>
+struct Run {
+  static constexpr int WORDS = VEC * (int)sizeof(T) / 4;
+  typedef typename std::conditional<WORDS == 4, u32x4_at2, typename std::conditional<WORDS == 2, u32x2_at2, u32x1_at2>::type>::type word;
   word u;
   __device__ __forceinline__ void load(const T* p) { u = *reinterpret_cast<const word*>(p); }
   __device__ __forceinline__ float get(int i) const {
@@ -61,17 +64,15 @@ struct Four {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void put_four(T* p, const float* v) {
-  typename Four<T>::word u;
-  if constexpr (sizeof(T) == 4) {
+template <int VEC, typename T>
+__device__ __forceinline__ void put_run(T* p, const float* v) {
+  typename Run<T, VEC>::word u;
 #pragma unroll
-    for (int i = 0; i < 4; i++) u[i] = __float_as_uint(v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; i++) u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < Run<T, VEC>::WORDS; i++) {
+    if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(v[i]);
+    else u[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
   }
-  *reinterpret_cast<typename Four<T>::word*>(p) = u;
+  *reinterpret_cast<typename Run<T, VEC>::word*>(p) = u;
 }
 __device__ __forceinline__ void put_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put_one(uint16_t* p, float v) { *p = f32_to_bf16(v); }
@@ -89,15 +90,15 @@ __device__ __forceinline__ T* head_at(T* row, uint32_t k) {
 template <typename T, int VEC, int LG, int C>
 struct HeadRow {
   static constexpr int N = VEC * C;
-  Four<T> a, b;           // VEC = 4
+  Run<T, VEC == 1 ? 4 : VEC> a, b;  // VEC > 1
   T one[VEC == 1 ? 2 * N : 1];
   __device__ __forceinline__ void load(const HeadLanes<VEC, LG, C>& l, const T* row, uint32_t k, bool on) {
-    if constexpr (VEC == 4) {
+    if constexpr (VEC > 1) {
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T); i++) a.u[i] = b.u[i] = 0;
+      for (int i = 0; i < Run<T, VEC>::WORDS; i++) a.u[i] = b.u[i] = 0;
       if (on && l.in(0)) {
         a.load(head_at(row, k + l.first(0)));
-        b.load(head_at(row, k + (l.beside() ? l.first(0) + 4 : l.second(0))));
+        b.load(head_at(row, k + (l.beside() ? l.first(0) + VEC : l.second(0))));
       }
     } else {
 #pragma unroll
@@ -111,12 +112,12 @@ struct HeadRow {
     }
   }
   __device__ __forceinline__ void get(const HeadLanes<VEC, LG, C>& l, float (&v)[2 * N]) const {
-    if constexpr (VEC == 4) {
+    if constexpr (VEC > 1) {
       const bool beside = l.beside();
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        v[i] = beside ? (i < 2 ? a.get(2 * i) : b.get(2 * i - 4)) : a.get(i);
-        v[4 + i] = beside ? (i < 2 ? a.get(2 * i + 1) : b.get(2 * i - 3)) : b.get(i);
+      for (int i = 0; i < VEC; i++) {
+        v[i] = beside ? (2 * i < VEC ? a.get(2 * i) : b.get(2 * i - VEC)) : a.get(i);
+        v[VEC + i] = beside ? (2 * i < VEC ? a.get(2 * i + 1) : b.get(2 * i + 1 - VEC)) : b.get(i);
       }
     } else {
 #pragma unroll
@@ -128,17 +129,17 @@ struct HeadRow {
 template <int VEC, int LG, int C, typename T>
 __device__ __forceinline__ void head_put(const HeadLanes<VEC, LG, C>& l, T* row, uint32_t k, const float (&v)[2 * VEC * C]) {
   constexpr int N = VEC * C;
-  if constexpr (VEC == 4) {
+  if constexpr (VEC > 1) {
     if (!l.in(0)) return;
     const bool beside = l.beside();
-    float a[4], b[4];
+    float a[VEC], b[VEC];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      a[i] = beside ? v[(i & 1) * 4 + i / 2] : v[i];
-      b[i] = beside ? v[(i & 1) * 4 + 2 + i / 2] : v[4 + i];
+    for (int i = 0; i < VEC; i++) {
+      a[i] = beside ? v[(i & 1) * VEC + i / 2] : v[i];
+      b[i] = beside ? v[(i & 1) * VEC + VEC / 2 + i / 2] : v[VEC + i];
     }
-    put_four(head_at(row, k + l.first(0)), a);
-    put_four(head_at(row, k + (beside ? l.first(0) + 4 : l.second(0))), b);
+    put_run<VEC>(head_at(row, k + l.first(0)), a);
+    put_run<VEC>(head_at(row, k + (beside ? l.first(0) + VEC : l.second(0))), b);
   } else {
 #pragma unroll
     for (int i = 0; i < N; i++)
@@ -166,7 +167,7 @@ struct HeadWeights {
       wide.get(l, v);
     } else if (dtype == 1) {
       HeadRow<_Float16, VEC, LG, C> half;
-      if constexpr (VEC == 4) {
+      if constexpr (VEC > 1) {
         half.a.u = narrow.a.u;
         half.b.u = narrow.b.u;
       } else {
@@ -515,12 +516,17 @@ template <typename F>
 void head_dispatch(const HeadArgs& a, F f) {
   auto by_lanes = [&](auto t) {
     using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     using Four = std::integral_constant<int, 4>;
     if (a.D % 8 == 0 && a.rot % 8 == 0) {
       if (a.D <= 64) f(t, Four{}, std::integral_constant<int, 8>{}, One{});
       else if (a.D <= 128) f(t, Four{}, std::integral_constant<int, 16>{}, One{});
       else if (a.D <= 256) f(t, Four{}, std::integral_constant<int, 32>{}, One{});
       else f(t, Four{}, std::integral_constant<int, 64>{}, One{});
+    } else if (a.D % 4 == 0 && a.D <= 256 && (a.interleaved || a.rot % 4 == 0)) {
+      if (a.D <= 64) f(t, Two{}, std::integral_constant<int, 16>{}, One{});
+      else if (a.D <= 128) f(t, Two{}, std::integral_constant<int, 32>{}, One{});
+      else f(t, Two{}, std::integral_constant<int, 64>{}, One{});
     } else if (a.D <= 128) {
       f(t, One{}, std::integral_constant<int, 64>{}, One{});
     } else {
@@ -546,7 +552,7 @@ hipError_t head_launch(const HeadArgs& a, Kind) {
   constexpr int KIND = Kind::value;
   head_dispatch(a, [&](auto t, auto vec, auto lg, auto c) {
     constexpr int LG = decltype(lg)::value, VEC = decltype(vec)::value, C = decltype(c)::value;
-    if constexpr (KIND < 0 || VEC == 1 || LG < 64) {  // a cache's heads have 256 channels at most
+    if constexpr (KIND < 0 || VEC < 4 || LG < 64) {  // a cache's heads have 256 channels at most
       constexpr int SLOTS = 64 / LG;
       const int rounds = ceil_div(a.q_heads, SLOTS) + ceil_div(a.k_heads, SLOTS) * (KIND < 0 ? 1 : 2);
       const int parts = head_parts(a.tokens, rounds, HEAD_WAVES);

@@ -108,6 +108,23 @@ def test_sizes(D, rot, interleaved, act, par):
     c.check_backward(c.backward())
 
 
+@pytest.mark.parametrize("D,rot", [(4, 0), (12, 8), (20, 20), (36, 34), (60, 12), (68, 64), (100, 96), (132, 132), (148, 10),
+                                   (180, 60), (252, 252), (256, 100), (260, 260)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("act,par", [("f32", "bf16"), ("bf16", "f32")])
+def test_multiples_of_four(D, rot, interleaved, act, par):
+    """Heads and rotations that four divides and eight does not, some parts of a wider output
+    that starts at an odd element."""
+    c = Case(70, 7, 3, D, rot, interleaved, act=act, par=par)
+    c.check_forward(c.forward())
+    c.check_backward(c.backward())
+    wide = torch.zeros(70, 10 * D + 3, device=DEV, dtype=DT[act])
+    q, k = wide[:, 1:1 + 7 * D].unflatten(1, (7, D)), wide[:, 2 + 7 * D:2 + 10 * D].unflatten(1, (3, D))
+    q.copy_(c.gx[0]), k.copy_(c.gx[1])
+    for got, want in zip(nq.head_norm(q, k, c.gpos if rot else None, c.norm), c.forward()):
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("T", [0, 1, 2, 5, 63, 300, 2100])
 @pytest.mark.parametrize("Hq,Hk", [(1, 1), (8, 1), (64, 8), (3, 0), (0, 5), (9, 3), (1, 40)])
 @pytest.mark.parametrize("D", [64, 100])
@@ -264,6 +281,22 @@ def test_write_is_norm_then_write(kind, D, rot, interleaved, act):
         a.data.fill_(7), b.data.fill_(7)
         slots = torch.randperm(96, device=DEV)[:T]
         slots[T // 2] = -1
+        q, k = c.forward()
+        nq.kv_write(k, v, a, slots)
+        got = nq.head_norm_write(*c.gx, v, c.gpos, c.norm, b, slots)
+        assert torch.equal(got, q) and torch.equal(a.data, b.data)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8", "int4"])
+@pytest.mark.parametrize("D,rot", [(64, 4), (96, 92), (128, 100), (192, 180), (256, 252)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_write_of_rotations_that_four_divides(kind, D, rot, interleaved):
+    for act in ("bf16", "f32"):
+        c = Case(70, 9, 5, D, rot, interleaved, act=act)
+        v = torch.randn(70, 5, D, device=DEV, generator=torch.Generator(device=DEV).manual_seed(D)).to(DT[act])
+        a, b = (nq.KvCache(6, 5, D, page=16, kind=kind, device=DEV) for _ in range(2))
+        a.data.fill_(7), b.data.fill_(7)
+        slots = torch.randperm(96, device=DEV)[:70]
         q, k = c.forward()
         nq.kv_write(k, v, a, slots)
         got = nq.head_norm_write(*c.gx, v, c.gpos, c.norm, b, slots)
