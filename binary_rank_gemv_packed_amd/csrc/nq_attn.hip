@@ -54,8 +54,8 @@ constexpr int attn_grid(int D, int kind, bool fine, bool narrow) {
   return kind == KV_INT4 && !fine && narrow && D <= 128 ? 768 : 512;
 }
 // Whether more than 16 query heads a key head go 32 at a time, so that the cache is read once for
-// them: 64 sequences of 4096 tokens, 32 heads of one key head, bf16 55.7 -> 40.7 us, 8 bits 37.7 ->
-// 32.2.  Not 4 bits, which wait for their vector instructions (35.8 and 35.3 us), nor FINE or more
+// them: 64 sequences of 4096 tokens, 32 heads of one key head, bf16 55.0 -> 40.0 us, 8 bits 38.4 ->
+// 32.3 (at that step).  Not 4 bits, which wait for their vector instructions (35.8 and 35.3), nor FINE or more
 // channels, which have no registers or shared memory for it.
 constexpr bool attn_two(int D, int kind, bool fine) { return D <= 128 && kind != KV_INT4 && !fine; }
 constexpr int ATTN_PAIR = 32;     // tokens of a wave's step: two tiles
@@ -854,14 +854,14 @@ constexpr float attn_unit_ns(int units) { return units < 120 ? 5500.0f + 62.5f *
 // What a token of a long unit costs, by the chip's times over 1024 to 2048 tokens, heads of 64 to
 // 256: bf16 5.0 to 16.6 ns (60 bytes a ns into a CU), codes with four waves 8.2 to 11.8, as long as an
 // access takes, with eight 5.0 to 10.1; FINE 8 bits 6.3 to 10.1, 15.4 with four waves, 4
-// bits 7.3 to 20, four waves 11 to 26.
+// bits 7.1 to 17.5, four waves 11 to 26.
 // Eight waves are for codes and as many units as there are CUs (16 x 1024 tokens of 8 bits 14.3 ->
 // 12.3 us, 8 x 1024 of 4 bits 16.8 -> 12.6); for up to 256 tokens (16 x 256: 7.3 -> 7.5 us), bf16 (16 x
 // 1024: 15.7 -> 16.3) and more units (64 x 512 of 8 bits 15.8 -> 16.5) four are faster.
 constexpr float attn_token_ns(int D, int kind, bool fine, bool wide) {
   if (kind == KV_BF16) return 1.0f + D / 16.5f;
   if (kind == KV_INT8) return wide ? (3.5f + D / 50.0f) * (fine ? 1.25f : 1.0f) : 7.0f + D / (fine ? 30.0f : 60.0f);
-  return wide ? fine ? D / 10.0f : 3.5f + D / 40.0f : 7.0f + D / (fine ? 13.0f : 60.0f);
+  return wide ? fine ? D / 11.0f : 3.5f + D / 40.0f : 7.0f + D / (fine ? 15.0f : 60.0f);
 }
 
 template <int D, int KIND, bool FINE, bool NARROW, int HT>
@@ -870,11 +870,12 @@ void attn_cut(const AttnArgs& a) {
   constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
   hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES, HT>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
   // Heads of a workgroup of the join: one where there are few, else as many as leave the
-  // longest unit (all tokens in one sequence) 64 parts a group at most.  With one head each
-  // 64 sequences of 64 heads take 11.9 us instead of 5.8.
+  // longest unit (all tokens in one sequence) 64 parts a group at most, and two at least.  With one
+  // head each 64 sequences of 64 heads take 11.9 us instead of 5.8, of 32 heads of one key head 10.0
+  // instead of 6.4.
   constexpr int SLOTS = 256 / (D / 4);
   const int most = ratio < 16 * HT ? ratio : 16 * HT, groups = (grid / units + 2 + 63) / 64;
-  int hb = a.B * a.q_heads <= 512 || groups >= SLOTS ? 1 : SLOTS / groups;
+  int hb = a.B * a.q_heads <= 512 ? 1 : groups > SLOTS / 2 ? 2 : SLOTS / groups;
   hb = hb < most ? hb : most;
   const int blocks = (most + hb - 1) / hb;
   hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, 16 * HT, hb, blocks);
