@@ -22,12 +22,12 @@
 // exactly, and 4-bit codes as c, for 24 times the sum of the weights would cost some of
 // the bits that are asked for.
 //
-// Bound by memory where sequences are long: 32 of up to 16384 tokens (675 MB of bf16) 118
-// us with the join, 5.7 TB/s, where a large copy moves 5.2 and reads alone 6.9; 131072 tokens
+// Bound by memory where sequences are long: 32 of up to 16384 tokens (675 MB of bf16) 111
+// us with the join, 6.1 TB/s, where a large copy moves 5.2 and reads alone 6.9; 131072 tokens
 // of 8 bits 55 us, of which the join and its launch are 7 and the way to the first keys
 // (lengths, places, tiles, one access behind the other) 4; of 4 bits 43 us, where vector
 // instructions take half of the cycles and a wave still waits for a third of its own.  Heads of
-// 192 and 256 with FINE keep one workgroup a CU (shared memory).
+// 256 with FINE keep one workgroup a CU (shared memory).
 #include "nq_common.h"
 #include "nq_internal.h"
 
