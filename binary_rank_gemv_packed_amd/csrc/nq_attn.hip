@@ -14,12 +14,13 @@
 //
 // Arithmetic.  Keys and values enter as bf16: held values, or whole numbers (exact),
 // whose scale multiplies the product of keys and queries in fp32 and, for values, the
-// weight.  4-bit codes enter as c + 24 (set into the mantissa of 16) and 24 times
-// the sum of what they are multiplied with is taken off by the same MFMA.  Scores, maximum, sum and
+// weight.  4-bit codes enter as c + 24 or c + 136 (set into the mantissa of 16 or 128) and as
+// many times the sum of what they are multiplied with is taken off by another MFMA, at a cost of
+// some 136 / 7 2^-24 of the result, where a weight's rounding is 2^-8.  Scores, maximum, sum and
 // output are fp32.  Weights are rounded to bf16 (2^-8 each, and the sum of bf16 values
 // is taken over the rounded ones, so that a token that outweighs the others is exact);
 // FINE, for fp32 queries or outputs, takes weights and queries as three bf16 pieces,
-// exactly, and 4-bit codes as c, for 24 times the sum of the weights would cost some of
+// exactly, and 4-bit codes as c / 16, for many times the sum of the weights would cost some of
 // the bits that are asked for.
 //
 // Bound by memory where sequences are long: 32 of up to 16384 tokens (675 MB of bf16) 111
@@ -78,19 +79,23 @@ __device__ __forceinline__ u32x2 bytes_bf16(uint32_t w) {
   for (int i = 0; i < 4; i++) f[i] = __float_as_uint((float)(int8_t)(w >> (8 * i)));
   return u32x2{high_halves(f[1], f[0]), high_halves(f[3], f[2])};
 }
-// Nibbles p and p + 4 as bf16 of 16 + nibble, in two instructions: the mask lies in a
-// scalar and 16 in a vector register, which is what the combined and-or takes (left to
-// itself the compiler makes two of it, with constants in the instruction).
+// Nibbles p and p + 4 as bf16 of 16 + nibble, in two instructions, or of 128 + nibble, where
+// nibble 0 needs no shift (131072 tokens 44.8 -> 43.4 us, 64 x 4096 73.9 -> 72.2): the masks lie in scalar and 16 and 128 in vector registers,
+// which is what the combined and-or takes (left to itself the compiler makes two of it, with
+// constants in the instruction).
 struct Nibbles {
-  uint32_t mask, sixteen;
+  uint32_t mask, sixteen, low, high;
   __device__ __forceinline__ Nibbles() {
     asm volatile("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+    asm volatile("s_mov_b32 %0, 0x000f000f" : "=s"(low));
     asm volatile("v_mov_b32 %0, 0x41804180" : "=v"(sixteen));
+    asm volatile("v_mov_b32 %0, 0x43004300" : "=v"(high));
   }
-  __device__ __forceinline__ uint32_t bf16(uint32_t w, int p) const {
-    return ((p == 0 ? w << 3 : w >> (4 * p - 3)) & mask) | sixteen;
-  }
+  __device__ __forceinline__ uint32_t from16(uint32_t w, int p) const { return (w >> (4 * p - 3) & mask) | sixteen; }
+  __device__ __forceinline__ uint32_t from128(uint32_t w, int p) const { return (w >> (4 * p) & low) | high; }
 };
+// What is taken off again of an operand's four words: 128 + 8 and 16 + 8.
+__device__ __forceinline__ u32x4 code_bias() { return u32x4{0xc308c308u, 0xc1c0c1c0u, 0xc308c308u, 0xc1c0c1c0u}; }
 // Nibbles p and p + 4 as bf16 of (nibble - 8) / 16: the conversion takes four bits as a signed
 // number and, where they lie at the bottom of a byte, needs no shift before it (1.75
 // instructions a code; with a shift, a mask, a conversion and a subtraction 3.1).
@@ -100,7 +105,6 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int p) {
   const float hi = __builtin_amdgcn_cvt_off_f32_i4((int)(s >> (p & 2 ? 24 : 16) & 255u));
   return high_halves(__float_as_uint(hi), __float_as_uint(lo));
 }
-constexpr uint32_t MINUS_24 = 0xc1c0c1c0u;  // two bf16
 
 // ------------------------------------------------------------------ which tokens
 // Pairs (of tiles, 32 tokens) of a sequence of n tokens that are seen: from first_pair()
@@ -254,7 +258,7 @@ struct Half {
     } else {
       const uint32_t u = w[i][c];
       if constexpr (FINE) return u32x4{codes_bf16(u, 0), codes_bf16(u, 1), codes_bf16(u, 2), codes_bf16(u, 3)};
-      return u32x4{nb.bf16(u, 0), nb.bf16(u, 1), nb.bf16(u, 2), nb.bf16(u, 3)};
+      return u32x4{nb.from128(u, 0), nb.from16(u, 1), nb.from128(u, 2), nb.from16(u, 3)};
     }
   }
   // values: operand of 16 channels of the pair; keep: the bits of bf16 values that are seen
@@ -269,7 +273,7 @@ struct Half {
       const int h = x & 1;
       const uint32_t a = w[0][x / 2], b = w[1][x / 2];
       if constexpr (FINE) return u32x4{codes_bf16(a, h), codes_bf16(a, 2 + h), codes_bf16(b, h), codes_bf16(b, 2 + h)};
-      return u32x4{nb.bf16(a, h), nb.bf16(a, 2 + h), nb.bf16(b, h), nb.bf16(b, 2 + h)};
+      return u32x4{nb.from128(a, h), nb.from16(a, 2 + h), nb.from128(b, h), nb.from16(b, 2 + h)};
     }
   }
 };
@@ -349,7 +353,7 @@ template <int D, int KIND, bool FINE, bool NARROW, int HT>
 struct Wave {
   static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE);
   static constexpr int TILES = NARROW ? 1 : 2, X = 4 * TILES;  // scores of a lane
-  static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24
+  static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24 or c + 136
   v4f o[HT][XT];
   float m[HT], safe[HT], l[HT];
   int lane;
@@ -369,7 +373,7 @@ struct Wave {
   // and of the sixteenth behind it)
   __device__ __forceinline__ void scores(const Half<D, KIND, false, NARROW>& t, const uint32_t (*q)[64][4], float c,
                                          float (&x)[HT][X]) const {
-    const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
+    const u32x4 minus = code_bias();
     v4f s[HT][2];
 #pragma unroll
     for (int h = 0; h < HT; h++) s[h][0] = s[h][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
@@ -476,8 +480,7 @@ struct Wave {
 #pragma unroll
           for (int i = PIECES - 1; i >= 0; i--) o[h][x] = mfma(value, w[h][i], o[h][x]);
           if constexpr (BIAS) {
-            const u32x4 minus = {MINUS_24, MINUS_24, MINUS_24, MINUS_24};
-            o[h][x] = mfma(minus, w[h][0], o[h][x]);
+            o[h][x] = mfma(code_bias(), w[h][0], o[h][x]);
           }
         }
       }
