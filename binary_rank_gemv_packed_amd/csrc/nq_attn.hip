@@ -48,11 +48,16 @@ typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int ATTN_WAVES = 4;
 // Workgroups that share the tokens of all sequences: as many as a chip of 256 CUs holds at
-// once.  Three a CU for bf16 results of 4-bit caches (up to eight query heads a key head),
-// whose registers allow it and whose vector and matrix instructions it overlaps (131072 tokens
-// 46.6 -> 43.6 us); two elsewhere: 8 bits 54.9 us against 57.7 with three, bf16 96.7 and 100.0.
+// once.  Three a CU where registers allow it and vector and matrix instructions are much of the time,
+// which it overlaps: codes of 64 channels (64 x 4096 tokens, 4 key heads, 8 bits 36.6 -> 33.3 us, 4 bits 31.7 ->
+// 29.8, with fp32 40.1 -> 38.1) and 4 bits for up to eight query heads a key head (131072 tokens of 8 x
+// 128 46.6 -> 43.6; 64 x 4096 of 4 x 96 with fp32 50.8 -> 48.4).  Two elsewhere: heads of 128 with 8 bits
+// 54.9 us, 57.7 with three, bf16 96.7 and 100.0, of 96 with 8 bits 43.4 and 43.3.  One for FINE heads of 256,
+// whose shared memory and registers fill a CU (8 x 4096 tokens of 8 bits 33.3 -> 24.6 us, of bf16 35.7 -> 32.0).
 constexpr int attn_grid(int D, int kind, bool fine, bool narrow) {
-  return kind == KV_INT4 && !fine && narrow && D <= 128 ? 768 : 512;
+  if (fine && D == 256) return 256;
+  if (kind != KV_BF16 && D == 64) return 768;
+  return kind == KV_INT4 && narrow && D <= (fine ? 96 : 128) ? 768 : 512;
 }
 // Whether more than 16 query heads a key head go 32 at a time, so that the cache is read once for
 // them: 64 sequences of 4096 tokens, 32 heads of one key head, bf16 55.0 -> 40.0 us, 8 bits 38.4 ->
@@ -177,7 +182,7 @@ struct Counts {
 
 // A workgroup's share of `total`: at least a pair a wave.
 __device__ __forceinline__ long long share_of(long long total, int grid) {
-  const long long even = (total + grid - 1) / grid;
+  const long long even = quotient(total + grid - 1, grid);
   return even < ATTN_WAVES ? ATTN_WAVES : even;
 }
 
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
   long long left;  // what this workgroup's share holds behind g
   if constexpr (SPLIT) {
     const Counts n(a, lengths);
-    const long long total = (long long)n.total * units, share = share_of(total, attn_grid(D, KIND, FINE, NARROW)), start = share * blockIdx.x;
+    const long long total = (long long)n.total * units, share = share_of(total, (int)gridDim.x), start = share * blockIdx.x;
     if (start >= total) return;
     left = total - start < share ? total - start : share;
     const bool here = start >= (long long)n.before * units && start < ((long long)n.before + n.mine) * units;
@@ -884,7 +889,13 @@ constexpr float attn_token_ns(int D, int kind, bool fine, bool wide) {
 template <int D, int KIND, bool FINE, bool NARROW, int HT>
 void attn_cut(const AttnArgs& a) {
   const int ratio = a.q_heads / a.cache.heads, units = a.cache.heads * head_tiles(ratio, 16 * HT);
-  constexpr int grid = attn_grid(D, KIND, FINE, NARROW);
+  // The third workgroup a CU is for long work: 32 units of 4096 tokens of 64 channels in 8 bits take
+  // 15.1 us with 512 workgroups and 15.6 with 768, of 16384 24.7 and 23.3; 14 of 33028 of 96 in 4 bits a
+  // step of 34.3 and 32.5.
+  const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
+  const bool little = (long long)a.B * units * longest < 8192LL * ATTN_PAIR;
+  constexpr int full = attn_grid(D, KIND, FINE, NARROW);
+  const int grid = full > 512 && little ? 512 : full;
   hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES, HT>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
   // Heads of a workgroup of the join: one where there are few, else as many as leave the
   // longest unit (all tokens in one sequence) 64 parts a group at most, and two at least.  With one
@@ -932,10 +943,14 @@ void attn_by_kind(const AttnArgs& a) {
 
 }  // namespace
 
-size_t attn_workspace(const KvLayout& l) {
-  const size_t one = attn_grid(l.D, l.kind, false, true) * slot_floats(l.D, 16);
-  const size_t two = attn_grid(l.D, l.kind, false, false) * slot_floats(l.D, 32);
-  return align_up((attn_two(l.D, l.kind, false) ? two : one) * 2 * 4, 256);
+size_t attn_workspace(const KvLayout& l) {  // two parts a workgroup, of what takes most
+  size_t most = 0;
+  for (int form = 0; form < 4; form++) {
+    const bool fine = form & 1, narrow = form & 2;
+    const size_t floats = attn_grid(l.D, l.kind, fine, narrow) * 2 * slot_floats(l.D, attn_two(l.D, l.kind, fine) ? 32 : 16);
+    most = floats > most ? floats : most;
+  }
+  return align_up(most * 4, 256);
 }
 
 hipError_t attn_forward(const AttnArgs& a) {
