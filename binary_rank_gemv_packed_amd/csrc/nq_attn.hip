@@ -181,8 +181,8 @@ struct Counts {
 };
 
 // A workgroup's share of `total`: at least a pair a wave.
-__device__ __forceinline__ long long share_of(long long total, int grid) {
-  const long long even = quotient(total + grid - 1, grid);
+__device__ __forceinline__ long long share_of(long long total, int grid) {  // 256, 512 or 768: no division
+  const long long t = total + grid - 1, even = grid == 768 ? t / 768 : grid == 512 ? t / 512 : t / 256;
   return even < ATTN_WAVES ? ATTN_WAVES : even;
 }
 
@@ -893,7 +893,7 @@ void attn_cut(const AttnArgs& a) {
   // 15.1 us with 512 workgroups and 15.6 with 768, of 16384 24.7 and 23.3; 14 of 33028 of 96 in 4 bits a
   // step of 34.3 and 32.5.
   const int longest = a.window > 0 && a.window < a.max_length ? a.window : a.max_length;
-  const bool little = (long long)a.B * units * longest < 8192LL * ATTN_PAIR;
+  const bool little = (long long)a.B * units * longest < 12288LL * ATTN_PAIR;
   constexpr int full = attn_grid(D, KIND, FINE, NARROW);
   const int grid = full > 512 && little ? 512 : full;
   hipLaunchKernelGGL((attn_kernel<D, KIND, FINE, NARROW, true, ATTN_WAVES, HT>), dim3(grid), dim3(64 * ATTN_WAVES), 0, a.stream, a);
