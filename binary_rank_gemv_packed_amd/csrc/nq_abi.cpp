@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1200,6 +1201,12 @@ nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_
     return fail(NQ_ERR_INVALID_ARG, "a table of %d pages a sequence holds no or more than 2^30 tokens", table_width);
   if (max_length < 0 || window < 0) return fail(NQ_ERR_INVALID_ARG, "max_length %d or window %d below zero", max_length, window);
   if (!std::isfinite(scale)) return fail(NQ_ERR_INVALID_ARG, "scale must be finite");
+  const int32_t holds = table_width * C->page, longest = max_length && max_length < holds ? max_length : holds;
+  // what the kernels count a sequence as at most: a window of w tokens touches (w + 62) / 32 steps of 32
+  const int32_t steps = window && window < longest ? std::min((longest + 31) / 32, (int32_t)(((int64_t)window + 62) / 32))
+                                                   : (longest + 31) / 32;
+  if ((int64_t)B * (steps + nq::ATTN_TURN) > INT32_MAX)
+    return fail(NQ_ERR_INVALID_ARG, "%d sequences of up to %d tokens, window %d: over 2^31 steps of 32 tokens", B, longest, window);
   if (B == 0) return ok();
   const int64_t width = (int64_t)q_heads * C->head_dim;
   st = check_rows("q", q, B, width, width, qb);
@@ -1230,10 +1237,7 @@ nq_status nq_kv_attention(const nq_kv_cache* C, int32_t B, const void* q, int32_
   a.table = table;
   a.table_width = table_width;
   a.lengths = lengths;
-  const int32_t holds = table_width * C->page;
-  a.max_length = max_length && max_length < holds ? max_length : holds;
-  if ((int64_t)B * (a.max_length / 32 + 8) > INT32_MAX)
-    return fail(NQ_ERR_INVALID_ARG, "%d sequences of up to %d tokens: over 2^36 in all", B, a.max_length);
+  a.max_length = longest;
   a.window = window;
   a.scale = scale;
   a.part = static_cast<float*>(workspace);

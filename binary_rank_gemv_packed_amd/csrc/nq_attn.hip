@@ -65,9 +65,9 @@ constexpr int attn_grid(int D, int kind, bool fine, bool narrow) {
 // channels, which have no registers or shared memory for it.
 constexpr bool attn_two(int D, int kind, bool fine) { return D <= 128 && kind != KV_INT4 && !fine; }
 constexpr int ATTN_PAIR = 32;     // tokens of a wave's step: two tiles
-// What a unit costs beside its pairs (its queries, places and the waves' join), in pairs:
-// 64 sequences of 256 to 4096 tokens of 8 bits 57.0 us counted as 0, 49.8 as 4, 46.9 as 8, 47.5 as 12.
-constexpr int ATTN_TURN = 8;
+// ATTN_TURN (nq_internal.h) is what a unit costs beside its pairs (its queries, places and the waves'
+// join), in pairs: 64 sequences of 256 to 4096 tokens of 8 bits 57.0 us counted as 0, 49.8 as 4, 46.9 as
+// 8, 47.5 as 12.
 constexpr float ATTN_RISE = 8.0f;  // a maximum is raised by more than this (powers of two)
 #define NEG_INF (-__builtin_inff())
 

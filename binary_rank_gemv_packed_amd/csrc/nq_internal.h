@@ -290,7 +290,9 @@ hipError_t head_forward(const HeadArgs& a);
 hipError_t head_write(const HeadArgs& a);
 hipError_t head_backward(const HeadArgs& a);
 
-// One token's attention over the paged cache (nq_attn.hip).
+// One token's attention over the paged cache (nq_attn.hip).  A sequence is counted as its
+// steps of 32 tokens and ATTN_TURN more; over all sequences the count stays below 2^31.
+constexpr int ATTN_TURN = 8;
 struct AttnArgs {
   KvLayout cache;
   const uint8_t* data;

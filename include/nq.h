@@ -437,6 +437,8 @@ nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots,
  *             0 gives zeros.  At most max_length, which is what the host knows of them (0, or
  *             more than the table holds: table_width * page); a length outside 0..max_length
  *             makes its sequence's outputs NaN
+ *             B times (steps of 32 tokens that a longest sequence has, of them those that its window
+ *             touches, and 8) has to stay below 2^31
  *   table   : device; entries of pages without a token that is seen are not read; a page
  *             outside the cache, where one is, makes outputs of its sequence NaN and is not read
  *   workspace : device, >= nq_kv_attention_workspace_bytes(C), 256-byte aligned; no initial contents
