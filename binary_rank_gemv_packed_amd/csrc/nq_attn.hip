@@ -192,6 +192,30 @@ __device__ __forceinline__ long long share_of(long long total, int grid) {  // 2
   return even < ATTN_WAVES ? ATTN_WAVES : even;
 }
 
+// The unit, and how far into its cost, that lies `start` into what all units cost: the units of
+// sequence b one after the other, b's behind those of all before it.
+struct Begin {
+  Span sp;
+  int b, unit, from;
+  // false: nothing there, which is not so while the lengths stay as they were counted
+  __device__ __forceinline__ bool find(const AttnArgs& a, const Counts& n, Lengths& lengths, int units, long long start) {
+    const bool here = start >= (long long)n.before * units && start < ((long long)n.before + n.mine) * units;
+    const int owner = __builtin_ctzll(__ballot(here));
+    b = owner * n.each;
+    long long rest = start - (long long)__builtin_amdgcn_readlane(n.before, owner) * units;
+    if (n.each > 1) lengths.load(a, b);
+    sp = lengths.span(a, b);
+    while (rest >= (long long)sp.cost() * units) {
+      rest -= (long long)sp.cost() * units;
+      if (++b >= a.B) return false;
+      sp = lengths.span(a, b);
+    }
+    unit = (int)quotient(rest, sp.cost());
+    from = (int)(rest - (long long)unit * sp.cost());
+    return true;
+  }
+};
+
 // Units of a key head's query heads, `cols` (16 or 32) each, and a part of one in the
 // workspace: sums [cols][D], maxima [cols], weights' sums [cols].
 __host__ __device__ inline int head_tiles(int ratio, int cols) { return (ratio + cols - 1) / cols; }
@@ -603,21 +627,10 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
     const long long total = (long long)n.total * units, share = share_of(total, (int)gridDim.x), start = share * blockIdx.x;
     if (start >= total) return;
     left = total - start < share ? total - start : share;
-    const bool here = start >= (long long)n.before * units && start < ((long long)n.before + n.mine) * units;
-    const int owner = __builtin_ctzll(__ballot(here));
-    int b = owner * n.each;
-    long long from = start - (long long)__builtin_amdgcn_readlane(n.before, owner) * units;
-    if (n.each > 1) lengths.load(a, b);
-    Span sp = lengths.span(a, b);
-    while (from >= (long long)sp.cost() * units) {
-      from -= (long long)sp.cost() * units;
-      if (++b >= a.B) return;  // not reached while the lengths stay as they were counted
-      sp = lengths.span(a, b);
-    }
-    const int unit = (int)quotient(from, sp.cost());
-    from -= (long long)unit * sp.cost();
-    g.at(sp, b, unit, (int)from, left);
-    left -= sp.cost() - from;
+    Begin to;
+    if (!to.find(a, n, lengths, units, start)) return;
+    g.at(to.sp, to.b, to.unit, to.from, left);
+    left -= to.sp.cost() - to.from;
     if (g.empty()) return;  // the share ends within what stands in front of its only unit
   } else {
     const int n = a.lengths[blockIdx.x / units];
@@ -790,33 +803,69 @@ __global__ void __launch_bounds__(64 * WAVES, WAVES / 4 > 2 ? WAVES / 4 : 2) att
 
 // Joins the parts of units that were cut, `hb` query heads of one unit a workgroup:
 // D / 4 threads go through the parts of a head that fall to their group of them, eight
-// parts in flight, and the groups' sums are added in order.
-template <int D>
+// parts in flight, and the groups' sums are added in order.  Sequences without tokens or
+// with a bad length are filled here.
+//
+// The workgroups are those of every unit, or with BORDERS those of every border of two shares, of
+// which the first in a unit joins it, and behind them one for each four sequences, a wave each.
+// A workgroup of either kind reads all lengths, so that the former takes time with the square of the
+// sequences and is for no more units than there are shares.  B sequences of 1 to 200 tokens and one of
+// 4096, 8 key heads of 128, 8 bits, the whole call with a workgroup a unit and with borders: B = 96 30.8
+// and 30.2 us, 128 34.0 and 31.6, 256 53.7 and 45.9, 1024 251 and 131, 4096 2244 and 408.
+template <int D, bool BORDERS>
 __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int grid, int cols, int hb, int blocks) {
   constexpr int Q = D / 4, SLOTS = 256 / Q, N = 8;
   __shared__ v4f sums[SLOTS][Q];
   __shared__ float slot_m[SLOTS], slot_l[SLOTS];
   const int heads = a.cache.heads, ratio = a.q_heads / heads, tiles = head_tiles(ratio, cols), units = heads * tiles;
-  const int b = blockIdx.y, unit = blockIdx.x / blocks, tid = threadIdx.x;
-  Lengths lengths;
-  const Counts n(a, lengths);
-  const int length = n.each > 1 ? a.lengths[b] : __builtin_amdgcn_readlane(lengths.held, b), pairs = span_of(a, length).pairs();
-  const int slot = tid / Q, d = tid % Q, groups = SLOTS / hb, group = slot / hb, col = blockIdx.x % blocks * hb + slot % hb;
-  const bool on = group < groups && col < cols && unit % tiles * cols + col < ratio;
-  const size_t at = ((size_t)b * a.q_heads + unit / tiles * ratio + unit % tiles * cols + col) * D + 4 * d;
-  auto put = [&](v4f y) {
+  const int tid = threadIdx.x;
+  auto put_at = [&](size_t at, v4f y) {
     if (a.y_dtype == 0) *reinterpret_cast<v4f*>(static_cast<float*>(a.y) + at) = y;
     else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.y) + at) = u32x2{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
   };
-  if (!pairs) {
-    const float y = bad_length(a, length) ? __uint_as_float(0x7fc00000u) : 0.0f;
+  auto nothing = [&](int length) { return bad_length(a, length) ? __uint_as_float(0x7fc00000u) : 0.0f; };
+  if (BORDERS && (int)blockIdx.x >= (grid - 1) * blocks) {
+    const int b = ((int)blockIdx.x - (grid - 1) * blocks) * 4 + (tid >> 6);
+    if (b >= a.B) return;
+    const int length = a.lengths[b];
+    if (span_of(a, length).pairs()) return;
+    const float y = nothing(length);
+    const int count = a.q_heads * D;
+    for (int i = 4 * (tid & 63); i < count; i += 256) put_at((size_t)b * count + i, v4f{y, y, y, y});
+    return;
+  }
+  Lengths lengths;
+  const Counts n(a, lengths);
+  const long long total = (long long)n.total * units, share = share_of(total, grid);
+  int b, unit, pairs, length = 0;
+  long long start;  // of the unit's pairs within what all units cost
+  if constexpr (BORDERS) {
+    const int border = blockIdx.x / blocks + 1;
+    Begin to;
+    if (share * border >= total || !to.find(a, n, lengths, units, share * border)) return;
+    b = to.b;
+    unit = to.unit;
+    pairs = to.sp.pairs();
+    start = share * border - to.from + ATTN_TURN;
+    if (quotient(start, share) != border - 1) return;  // cut further in front, or here before its first pair
+  } else {
+    b = blockIdx.y;
+    unit = blockIdx.x / blocks;
+    length = n.each > 1 ? a.lengths[b] : __builtin_amdgcn_readlane(lengths.held, b);
+    pairs = span_of(a, length).pairs();
+    int front = __builtin_amdgcn_readlane(n.before, b / n.each);
+    for (int i = b / n.each * n.each; i < b; i++) front += span_of(a, a.lengths[i]).cost();
+    start = (long long)front * units + (long long)unit * (pairs + ATTN_TURN) + ATTN_TURN;
+  }
+  const int slot = tid / Q, d = tid % Q, groups = SLOTS / hb, group = slot / hb, col = blockIdx.x % blocks * hb + slot % hb;
+  const bool on = group < groups && col < cols && unit % tiles * cols + col < ratio;
+  const size_t at = ((size_t)b * a.q_heads + unit / tiles * ratio + unit % tiles * cols + col) * D + 4 * d;
+  auto put = [&](v4f y) { put_at(at, y); };
+  if (!BORDERS && !pairs) {
+    const float y = nothing(length);
     if (on && group == 0) put(v4f{y, y, y, y});
     return;
   }
-  int front = __builtin_amdgcn_readlane(n.before, b / n.each);
-  for (int i = b / n.each * n.each; i < b; i++) front += span_of(a, a.lengths[i]).cost();
-  const long long share = share_of((long long)n.total * units, grid);
-  const long long start = (long long)front * units + (long long)unit * (pairs + ATTN_TURN) + ATTN_TURN;
   const int w0 = (int)quotient(start, share), w1 = (int)quotient(start + pairs - 1, share), parts = w1 - w0 + 1;
   if (parts == 1 || w1 >= grid) return;  // the latter not while the lengths stay as they were counted
   float m = NEG_INF, l = 0.0f;
@@ -912,7 +961,12 @@ void attn_cut(const AttnArgs& a) {
   int hb = a.B * a.q_heads <= 512 ? 1 : groups > SLOTS / 2 ? 2 : SLOTS / groups;
   hb = hb < most ? hb : most;
   const int blocks = (most + hb - 1) / hb;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, 16 * HT, hb, blocks);
+  if ((long long)a.B * units > grid) {
+    const dim3 all((unsigned)((grid - 1) * blocks + (a.B + 3) / 4));
+    hipLaunchKernelGGL((attn_join_kernel<D, true>), all, dim3(256), 0, a.stream, a, grid, 16 * HT, hb, blocks);
+  } else {
+    hipLaunchKernelGGL((attn_join_kernel<D, false>), dim3(units * blocks, a.B), dim3(256), 0, a.stream, a, grid, 16 * HT, hb, blocks);
+  }
 }
 
 template <int D, int KIND, bool FINE, bool NARROW>
