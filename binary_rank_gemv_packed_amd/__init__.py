@@ -27,6 +27,7 @@ NQ_ENVELOPE_MAX = 4  # terms of a rank-l envelope (include/nq.h)
 NQ_NORM_POST, NQ_NORM_PRE, NQ_NORM_MAX_DIM = 1, 2, 32768  # block norms (include/nq.h)
 NQ_HEAD_NORM, NQ_HEAD_INTERLEAVED, NQ_HEAD_MAX_AXES = 1, 2, 4  # head norms (include/nq.h)
 KV_KINDS = {"bf16": 0, "int8": 1, "int4": 2}  # how a cache holds its values (include/nq.h)
+_INT32_MAX = 2 ** 31 - 1  # more than a call's tokens: ctypes would cut a wider whole number to its lower bits
 PATHS = {"auto": 0, "gemv": 1, "gemm": 2, "valu": 3, "decode": 4}
 
 _DT = {torch.float32: NQ_F32, torch.float16: NQ_F16, torch.bfloat16: NQ_BF16}
@@ -838,9 +839,11 @@ def kv_attention_into(q: torch.Tensor, cache: KvCache, table: torch.Tensor, leng
     _gpu_tensor(table, "table", torch.int32, (B, table.shape[1]), dev)
     _scratch(workspace, dev)
     scale = cache.head_dim ** -0.5 if scale is None else scale
+    if window < 0 or max_length < 0:
+        raise NQError(NQ_ERR_INVALID_ARG, f"max_length {max_length} or window {window} below zero")
     _on_stream(dev, stream, lambda s: _check(lib().nq_kv_attention(
         cache.ref, B, q.data_ptr(), _DT[q.dtype], q_heads, table.data_ptr(), table.shape[1], lengths.data_ptr(),
-        max_length, window, scale, y.data_ptr(), _DT[y.dtype], workspace.data_ptr(), workspace.numel(), s)))
+        min(max_length, _INT32_MAX), min(window, _INT32_MAX), scale, y.data_ptr(), _DT[y.dtype], workspace.data_ptr(), workspace.numel(), s)))
     return y
 
 
