@@ -859,7 +859,7 @@ def kv_attention(q: torch.Tensor, cache: KvCache, table: torch.Tensor, lengths: 
     of 0, NaN for one above max_length (what the host knows of the lengths; 0: what the
     table holds) or a page outside the cache."""
     def call(_):
-        ws = workspace if workspace is not None else new_kv_workspace(q.shape[0], q.shape[1], cache)
+        ws = workspace if workspace is not None else new_kv_workspace(0, 0, cache)  # of any batch; q is checked below
         return kv_attention_into(q, cache, table, lengths, _like(q, out_dtype), ws, scale, window,
                                  max_length)
 

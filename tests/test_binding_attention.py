@@ -1,5 +1,5 @@
-"""Binding of the attention over the cache: numbers that do not fit the C ABI's 32 bits, on
-the host with stand-ins for GPU tensors."""
+"""Binding of the attention over the cache: numbers that do not fit the C ABI's 32 bits, and
+queries of a wrong rank, on the host with stand-ins for GPU tensors."""
 import pytest
 import torch
 
@@ -40,4 +40,12 @@ def test_below_zero_is_refused(calls, given):
     for kw in (dict(window=given), dict(max_length=given)):
         with pytest.raises(nq.NQError):
             attend(**kw)
+    assert not calls
+
+def test_queries_of_a_wrong_rank_are_refused(calls, monkeypatch):
+    monkeypatch.setattr(nq, "new_kv_workspace", lambda B, q_heads, cache: Stand((64 * MB,), U8))
+    monkeypatch.setattr(nq, "_like", lambda t, dtype=None: t)
+    for shape in ((), (256,), (2, 256), (1, 2, 4, 64)):
+        with pytest.raises(nq.NQError):
+            nq.kv_attention(Stand(shape, T_BF), held_cache(), Stand((2, 3), I32), Stand((2,), I32))
     assert not calls
