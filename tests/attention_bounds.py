@@ -77,8 +77,14 @@ def emulate(q, k, v, kind, scale, round_q=False, round_p=False):
     return mix(p, hv)
 
 
-def sequence(rng, n, H, D, loud=1.0, Hq=8):
-    """Queries, keys and values as they come: normal, values not about zero."""
-    q = (loud * rng.standard_normal((Hq, D))).astype(np.float32)
-    k = rng.standard_normal((n, H, D)).astype(np.float32)
-    return q, k, (rng.standard_normal((n, H, D)) + 0.25).astype(np.float32)
+def sequence(rng, n, H, D, loud=1.0, Hq=8, few=6):
+    """Queries, keys and values: normal, values not about zero.  The queries of a key head have a
+    direction in common, and `few` tokens anywhere a score about 12 above the others: what is
+    lost of a score or weight is then not evened out over many tokens."""
+    common = np.repeat(rng.standard_normal((H, D)), Hq // H, axis=0)
+    q = loud * (rng.standard_normal((Hq, D)) + 2 * common)
+    k = rng.standard_normal((n, H, D))
+    up = rng.choice(n, min(few, n), replace=False)
+    k[up] += 12.0 / (D ** -0.5 * loud * 2 * D) * common[::Hq // H]
+    v = rng.standard_normal((n, H, D)) + 0.25
+    return q.astype(np.float32), k.astype(np.float32), v.astype(np.float32)

@@ -26,10 +26,10 @@ def rising(n, D, seed, up, large):
     return q, k, v
 
 
-def attend(seqs, kind, q, y, page=32, **kw):
-    D = seqs[0][1].shape[2]
+def attend(seqs, kind, q, y, page=32, scale=float(np.log(2.0)), **kw):
+    H, D = seqs[0][1].shape[1:]
     need = [-(-len(s[1]) // page) for s in seqs]
-    cache = nq.KvCache(sum(need), 2, D, page=page, kind=kind, device=DEV)
+    cache = nq.KvCache(sum(need), H, D, page=page, kind=kind, device=DEV)
     cache.data.fill_(0xFF)
     table = np.zeros((len(seqs), max(need)), np.int32)
     slots, at = [], 0
@@ -41,7 +41,7 @@ def attend(seqs, kind, q, y, page=32, **kw):
     nq.kv_write(k, v, cache, torch.from_numpy(np.concatenate(slots)).to(DEV))
     lengths = torch.tensor([len(s[1]) for s in seqs], dtype=torch.int32, device=DEV)
     out = nq.kv_attention(torch.from_numpy(np.stack([s[0] for s in seqs])).to(DEV, q), cache, torch.from_numpy(table).to(DEV),
-                          lengths, scale=float(np.log(2.0)), out_dtype=y, **kw)
+                          lengths, scale=scale, out_dtype=y, **kw)
     return out.double().cpu().numpy()
 
 
