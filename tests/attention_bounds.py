@@ -25,13 +25,14 @@ from oracle import nq_kv as O
 E = 2.0 ** -24
 
 
-def softmax(q, k, scale):
-    """(heads, n) weights and largest scale * sum |q k| of a head, q (Hq, D), k (n, H, D)."""
+def softmax(q, k, scale, times=None):
+    """(heads, n) weights and largest scale * sum |q k| of a head, q (Hq, D), k (n, H, D), token t
+    there times[t] times."""
     H = k.shape[1]
     r = q.shape[0] // H
     x = np.concatenate([scale * (q[h * r:(h + 1) * r] @ k[:, h].T) for h in range(H)])
     big = np.concatenate([abs(scale) * (np.abs(q[h * r:(h + 1) * r]) @ np.abs(k[:, h]).T) for h in range(H)])
-    p = np.exp(x - x.max(axis=1, keepdims=True))
+    p = np.exp(x - x.max(axis=1, keepdims=True)) * (1.0 if times is None else times)
     return p / p.sum(axis=1, keepdims=True), big.max(axis=1, keepdims=True)
 
 
@@ -41,15 +42,16 @@ def mix(p, v):
     return np.concatenate([p[h * r:(h + 1) * r] @ v[:, h] for h in range(v.shape[1])])
 
 
-def expected(q, k, v, kind, scale, window=0, fine=False, out=torch.float32):
+def expected(q, k, v, kind, scale, window=0, fine=False, out=torch.float32, times=None):
     """(values, bound) of one sequence: q (Hq, D) as the call has it, k and v (n, H, D) fp32 as
-    they were written."""
+    they were written; times: how often it has each token (once)."""
     q = np.asarray(q, np.float64)
     if window:
         k, v = k[max(0, len(k) - window):], v[max(0, len(v) - window):]
-    n, H, D = k.shape
+    H, D = k.shape[1:]
+    n = len(k) if times is None else int(np.sum(times))
     hk, hv = O.held(k, kind), O.held(v, kind)
-    p, big = softmax(q, hk, scale)
+    p, big = softmax(q, hk, scale, times)
     y, mag = mix(p, hv), mix(p, np.abs(hv))
     d = (D + 16) * E * big
     bias = 0.0
