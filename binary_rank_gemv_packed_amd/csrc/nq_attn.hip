@@ -17,13 +17,18 @@
 // Arithmetic.  Keys and values enter as bf16: held values, or whole numbers (exact),
 // whose scale multiplies the product of keys and queries in fp32 and, for values, the
 // weight.  4-bit codes enter as c + 24 or c + 136 (set into the mantissa of 16 or 128) and as
-// many times the sum of what they are multiplied with is taken off by another MFMA, at a cost of
-// some 136 / 7 2^-24 of the result, where a weight's rounding is 2^-8.  Scores, maximum, sum and
-// output are fp32.  Weights are rounded to bf16 (2^-8 each, and the sum of bf16 values
-// is taken over the rounded ones, so that a token that outweighs the others is exact);
-// FINE, for fp32 queries or outputs, takes weights and queries as three bf16 pieces,
-// exactly, and 4-bit codes as c / 16, for many times the sum of the weights would cost some of
-// the bits that are asked for.
+// many times the sum of what they are multiplied with is taken off by another MFMA: both products
+// are rounded at the size of 144 s sum |q| (values: 144 s times the weights), an instruction's few
+// roundings of 2^-24 of that, which is 21 times what a group's largest code makes of it and so some
+// 2^-18 of such a score or value, whatever the result is, where a weight's rounding is 2^-8 of its
+// value.  Scores, maximum, sum and output are fp32.  Weights (with codes times their scale) enter as two
+// bf16 pieces, off by 2^-16, so that a bf16 output is off by its own rounding: with one, 2^-8 each,
+// the error of 131072 tokens was 2.2e-3 where the output's rounding is 1.7e-3 (8 bits 55.1 -> 55.6 us; 64 x
+// 4096 of 4 key heads of 64 35.8 -> 38.1, of 96 and more within 2 %, bf16 within 1 %, heads of 256 59.4 ->
+// 61.3).  For 4 bits one piece, which is far below their own step: two cost them a tenth (131072 tokens 42.3
+// -> 46.0 us, 64 x 4096 75 -> 83).  FINE, for fp32 queries or outputs, takes weights and queries as three
+// bf16 pieces, exactly, and 4-bit codes as c / 16, for many times the sum of the weights would
+// cost some of the bits that are asked for.
 //
 // Bound by memory where sequences are long: 32 of up to 16384 tokens (675 MB of bf16) 111
 // us with the join, 6.1 TB/s, where a large copy moves 5.2 and reads alone 6.9; 131072 tokens
@@ -386,8 +391,8 @@ __device__ __forceinline__ uint32_t eight_on(uint32_t v) {
 
 template <int D, int KIND, bool FINE, bool NARROW, int HT>
 struct Wave {
-  static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE);
-  static constexpr int TILES = NARROW ? 1 : 2, X = 4 * TILES;  // scores of a lane
+  static constexpr int CH = D / 32, XT = D / 16, NG = kv_groups(KIND, D), PIECES = query_pieces(FINE), WP = FINE ? 3 : KIND == KV_INT4 ? 1 : 2;
+  static constexpr int TILES = NARROW ? 1 : 2, X = 4 * TILES;  // scores of a lane; WP: pieces of a weight
   static constexpr bool BIAS = KIND == KV_INT4 && !FINE;  // codes enter as c + 24 or c + 136
   v4f o[HT][XT];
   float m[HT], safe[HT], l[HT];
@@ -494,7 +499,7 @@ struct Wave {
     constexpr int GROUPS = NG ? NG : 1;
 #pragma unroll
     for (int g = 0; g < GROUPS; g++) {
-      u32x4 w[HT][PIECES];
+      u32x4 w[HT][WP];
 #pragma unroll
       for (int h = 0; h < HT; h++) {
         float ps[X];
@@ -504,7 +509,7 @@ struct Wave {
         if (g == 0) {
 #pragma unroll
           for (int j = 0; j < X / 2; j++)
-            l[h] += NG || FINE ? p[h][2 * j] + p[h][2 * j + 1] : low_f32(w[h][0][j]) + high_f32(w[h][0][j]);
+            l[h] += p[h][2 * j] + p[h][2 * j + 1];
         }
       }
 #pragma unroll
@@ -513,9 +518,10 @@ struct Wave {
 #pragma unroll
         for (int h = 0; h < HT; h++) {
 #pragma unroll
-          for (int i = PIECES - 1; i >= 0; i--) o[h][x] = mfma(value, w[h][i], o[h][x]);
+          for (int i = WP - 1; i >= 0; i--) o[h][x] = mfma(value, w[h][i], o[h][x]);
           if constexpr (BIAS) {
-            o[h][x] = mfma(code_bias(), w[h][0], o[h][x]);
+#pragma unroll
+            for (int i = 0; i < WP; i++) o[h][x] = mfma(code_bias(), w[h][i], o[h][x]);
           }
         }
       }
@@ -523,12 +529,12 @@ struct Wave {
   }
 
   // weights as bf16, or as pieces that add up to them
-  __device__ __forceinline__ static void weights(const float (&p)[X], u32x4 (&w)[PIECES]) {
+  __device__ __forceinline__ static void weights(const float (&p)[X], u32x4 (&w)[WP]) {
 #pragma unroll
     for (int j = 0; j < X / 2; j++) {
       float lo = p[2 * j], hi = p[2 * j + 1];
 #pragma unroll
-      for (int i = 0; i < PIECES; i++) {
+      for (int i = 0; i < WP; i++) {
         w[i][j] = pack_bf16(lo, hi);
         lo -= low_f32(w[i][j]);
         hi -= high_f32(w[i][j]);

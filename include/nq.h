@@ -442,10 +442,11 @@ nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots,
  *   table   : device; entries of pages without a token that is seen are not read; a page
  *             outside the cache, where one is, makes outputs of its sequence NaN and is not read
  *   workspace : device, >= nq_kv_attention_workspace_bytes(C), 256-byte aligned; no initial contents
- * Scores, softmax statistics and sums are fp32; weights of the softmax are rounded to
- * bf16 (2^-8) for bf16 q and y, else not.  Sums are finite where n |v| is, for a 4-bit cache with bf16 q
- * and y (n + 700) |v|; sums of 143 |q| over 32 channels of a 4-bit cache have to be finite for bf16
- * q and y too.  Values whose size is below 2^-95 lose bits.  What lies in slots that are not seen
+ * Scores, softmax statistics and sums are fp32.  For bf16 q and y the weights of the softmax
+ * are rounded to 16 bits (2^-16), over a 4-bit cache to 8 (2^-8); else not.  Sums are finite where
+ * n |v| is, for a 4-bit cache with bf16 q and y (n + 700) |v|; there sums of 143 |q| over 32
+ * channels have to be finite too.  Values whose size is below 2^-95 lose bits.  What lies in slots
+ * that are not seen
  * does not matter.  Asynchronous on `stream`, capturable (lengths and table are read by
  * the kernels); calls that overlap in time need workspaces of their own; repeated calls
  * give identical bits.  B == 0 launches nothing.  B, max_length and the window choose

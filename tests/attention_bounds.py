@@ -10,9 +10,9 @@ With e = 2^-24, x the scores, P the softmax's weights, M = sum P |v| over held v
             up to 32 times each, at the size of scale s sum 144 |q|: 64 e of that.
   weights   off by d = the scores' error, and 2^-22 for the subtraction and the exponential; the
             sum of n weights by n / 32 + 64 roundings.  Numerator and denominator: twice d + 2^-22.
-  rounding  bf16 q and y: a weight (codes: weight times scale) has 8 significant bits, half a step
-            2^-8; a bf16 cache's sum is over the rounded ones, so the quotient has it once for M and once
-            for |y|.  fp32 q or y: three pieces, off by 2^-23 at most.
+  rounding  bf16 q and y: a weight (codes: weight times scale) comes as two bf16 pieces of 8
+            significant bits, half a step 2^-8 each, so it is off by 2^-16; over 4 bits as one, off by
+            2^-8.  fp32 q or y: three pieces, off by 2^-23 at most.
   values    4 bits with bf16 q and y: as the scores, 64 e of sum P s 144.
   output    half a step of its type."""
 from __future__ import annotations
@@ -61,10 +61,8 @@ def expected(q, k, v, kind, scale, window=0, fine=False, out=torch.float32, time
         d = d + 64 * E * 144 * abs(scale) * np.concatenate(
             [(np.abs(q[h * r:(h + 1) * r]) @ sk[:, h].T).max(axis=1, keepdims=True) for h in range(H)])
         bias = 64 * E * 144 * mix(p, sv)
-    w = 2.0 ** -23 if fine else 2.0 ** -8
+    w = 2.0 ** -23 if fine else 2.0 ** -8 if kind == "int4" else 2.0 ** -16
     tol = (2 * (2 * d + 2.0 ** -22) + w + (n / 32 + 64) * E) * mag + bias
-    if kind == "bf16" and not fine:
-        tol = tol + w * np.abs(y)
     return y, tol + torch.finfo(out).eps / 2 * (np.abs(y) + tol) + 1e-42
 
 

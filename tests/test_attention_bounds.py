@@ -43,6 +43,8 @@ def test_what_is_rejected(D, kind, loud, n):
     for w, t in ((want, tol), (low, wide)):
         assert rejected(np.zeros_like(w), w, t)
         assert rejected(mean, w, t)
+    if kind != "int4" and loud < 1:
+        assert rejected(O.bf16(B.emulate(bq, k, v, kind, scale, round_p=True).astype(np.float32)), low, wide)
     if kind == "int4":  # codes 8 too large, keys' or values'
         more = lambda x: O.held(x, kind) + 8 * np.repeat(O.scales(x, kind).astype(np.float64), 32, axis=-1)
         assert rejected(B.mix(B.softmax(bq.astype(np.float64), more(k), scale)[0], hv), low, wide)
