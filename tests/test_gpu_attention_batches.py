@@ -103,3 +103,33 @@ def test_all_long_all_short_and_hardly_any():
 
 def test_the_most_sequences_a_call_may_have():
     Shared(2, 64, "int4").check(mixed(65535, long=30), 4, F32, F32)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4"])
+def test_captured_and_replayed_while_sequences_come_and_go(kind):
+    """One captured call of a large batch over lengths that change between the replays, on a
+    workspace that eager calls use in between."""
+    s = Shared(8, 64, kind)
+    n = 200
+    rng = np.random.default_rng(3)
+    q = torch.randn((n, 8, 64), device=DEV).bfloat16()
+    table = torch.from_numpy(rng.integers(0, PAGES, (n, WIDTH)).astype(np.int32)).to(DEV)
+    lengths, ws, out = torch.zeros(n, dtype=torch.int32, device=DEV), nq.new_kv_workspace(n, 8, s.cache), torch.empty_like(q)
+    side = torch.cuda.Stream()
+
+    def call():
+        return nq.kv_attention_into(q, s.cache, table, lengths, out, ws)
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    for now in (mixed(n, 1), mixed(n, 2), np.zeros(n), np.full(n, WIDTH * PAGE), np.ones(n), mixed(n, 3)):
+        lengths.copy_(torch.from_numpy(now.astype(np.int32)))
+        want = call().clone()
+        ws.fill_(0xFF), out.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.uint8), want.view(torch.uint8))
