@@ -34,7 +34,7 @@
 // us with the join, 6.1 TB/s, where a large copy moves 5.2 and reads alone 6.9; 131072 tokens
 // of 8 bits 55 us, of which the join and its launch are 7 and the way to the first keys
 // (lengths, places, tiles, one access behind the other) 4; of 4 bits 43 us, where vector
-// instructions take half of the cycles and a wave still waits for a third of its own.  Heads of
+// instructions take half of the cycles and a wave still waits for two fifths of its own.  Heads of
 // 256 with FINE keep one workgroup a CU (shared memory).
 #include "nq_common.h"
 #include "nq_internal.h"

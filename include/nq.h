@@ -412,7 +412,7 @@ typedef struct {
 /* Bytes of one page; 0 for invalid arguments. */
 size_t nq_kv_page_bytes(int32_t heads, int32_t head_dim, int32_t page, int32_t kind);
 
-/* Writes `tokens` tokens: row t of k and v (heads x head_dim contiguous, rows
+/* Writes `tokens` tokens (up to 2^20): row t of k and v (heads x head_dim contiguous, rows
  * k_stride and v_stride elements apart, dtype NQ_BF16 or NQ_F32, aligned to the element) to slot
  * slots[t].  Slots outside the cache (negative ones, say) are left out; a slot
  * given twice holds either token, or parts of both.  Nothing else of a page
@@ -420,7 +420,7 @@ size_t nq_kv_page_bytes(int32_t heads, int32_t head_dim, int32_t page, int32_t k
 nq_status nq_kv_write(const nq_kv_cache* C, int32_t tokens, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int32_t dtype, const int64_t* slots, nq_stream_t stream);
 
-/* Reads slots back: k_out and v_out (tokens x heads x head_dim, contiguous) are
+/* Reads up to 2^20 slots back: k_out and v_out (tokens x heads x head_dim, contiguous) are
  * the held values, rounded once to dtype; zeros for a slot outside the cache. */
 nq_status nq_kv_read(const nq_kv_cache* C, int32_t tokens, const int64_t* slots, void* k_out, void* v_out,
                      int32_t dtype, nq_stream_t stream);
@@ -487,7 +487,7 @@ typedef struct {
   const double* inv_freq; /* device, rot / 2; angles are formed in 64 bits            */
 } nq_head_norm;
 
-/* Forward.  Row t of q holds q_heads x head_dim contiguous elements, rows q_stride
+/* Forward of up to 2^20 tokens and 1024 heads of q and of k.  Row t of q holds q_heads x head_dim contiguous elements, rows q_stride
  * elements apart (a part of a wider linear's output), k likewise; q_out and k_out are
  * contiguous and may be q and k themselves where those are.  q_heads or k_heads may be 0
  * (the pointers may then be NULL).  positions: device, axes x tokens, below 2^53 in
