@@ -33,7 +33,7 @@ def scattered(rng, n, T):
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("D", DIMS)
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("H,page,n,T", [(64, 48, 16 * 48, 259), (5, 16, 384 * 16, 3301)])
+@pytest.mark.parametrize("H,page,n,T", [(64, 48, 10 * 48, 257), (5, 16, 340 * 16, 3301)])
 def test_prompts(kind, D, dtype, H, page, n, T):
     """More than 16384 heads of tokens: a number of heads that is no power of two, a last group
     of four that is not full, slots in runs, single and left out, over an older filling."""
